@@ -358,6 +358,101 @@ QKN_API qkn_status flashnorm_proj_noalloc(const void *x, const void *W_folded, v
                                           float eps, void *stream);
 
 /*
+ * Rotary positions
+ * ----------------
+ * rotary_apply, qknorm_rotary and qknorm_rotary_backward turn parts of query
+ * and key rows by their token's position.  A row is a whole number of heads
+ * of head_dim elements; in each head the first rotary_dim elements (even, at
+ * most 1024 and at most head_dim) form rotary_dim / 2 pairs, the rest is left
+ * as it is.  Pair i of token t turns by theta = positions[t] * inv_freq[i]:
+ *   c = mscale * cos(theta), s = mscale * sin(theta)
+ *   y_a = x_a c - x_b s,  y_b = x_b c + x_a s
+ * The angle is formed in fp64 and reduced to less than a turn before cos and
+ * sin are taken in fp32: its error is 2^-52 of the angle before the
+ * reduction, less than fp32 resolves up to 10^8 radians.  No table is read or
+ * kept.
+ *
+ * positions  [T] int32 (pos_bits 32) or int64 (64), any values, in any order
+ * inv_freq   [rotary_dim / 2] fp64, radians per position.  Frequencies that
+ *            are scaled for longer contexts are given here as they are
+ * mscale     finite factor on cos and sin (1 unless the scaling asks for one)
+ * layout     which two elements of a head form pair i
+ */
+typedef enum {
+    QKN_ROTARY_HALF = 0,        /* i and i + rotary_dim / 2 */
+    QKN_ROTARY_INTERLEAVED = 1  /* 2i and 2i + 1 */
+} qkn_rotary_layout;
+
+/*
+ * rotary_apply -- rotary positions on query and key rows (one launch).
+ *
+ * No counterpart in the pages, which stop at QK-Norm; in a block the
+ * normalised q and k take their positions next.
+ *
+ * q [T][dq], k [T][dk], pitches ldq, ldk; dk == 0 rotates q only.  q_out ==
+ * NULL (resp. k_out == NULL) works in place.  inverse != 0 turns back (the
+ * sine's sign is flipped, mscale is still applied): the gradient of the call
+ * without it.  fp32 arithmetic, one rounding to `act`.  Any element-aligned
+ * pointers and pitches are accepted; 16-byte aligned rows with head_dim a
+ * multiple of 16 bytes and rotary_dim of 32 bytes take the fast kernel.
+ */
+QKN_API qkn_status rotary_apply(const void *q, const void *k, void *q_out, void *k_out,
+                                int64_t T, int64_t dq, int64_t dk,
+                                int64_t ldq, int64_t ldk, int64_t ldq_out, int64_t ldk_out,
+                                int64_t head_dim, const void *positions, int pos_bits,
+                                const double *inv_freq, int64_t rotary_dim,
+                                qkn_rotary_layout layout, float mscale, int inverse,
+                                qkn_dtype act, void *stream);
+
+/*
+ * qknorm_rotary -- QK-Norm of the full query and key rows (as qknorm_fused
+ * with n_seg = 1) followed by rotary positions, in one pass over the rows:
+ *   n = (x * rsqrt(mean(x^2) + eps)) * w,  y = rotary(n)
+ * n is not rounded in between; y is rounded once.  rotary_dim == 0 leaves the
+ * rotation out (head_dim, positions, pos_bits, inv_freq, layout and mscale
+ * are then ignored).  Arguments as for qknorm_fused and rotary_apply.
+ */
+QKN_API qkn_status qknorm_rotary(const void *q, const void *k, const void *wq, const void *wk,
+                                 void *q_out, void *k_out, int64_t T, int64_t dq, int64_t dk,
+                                 int64_t ldq, int64_t ldk, int64_t ldq_out, int64_t ldk_out,
+                                 int64_t head_dim, const void *positions, int pos_bits,
+                                 const double *inv_freq, int64_t rotary_dim,
+                                 qkn_rotary_layout layout, float mscale,
+                                 qkn_dtype act, qkn_dtype wdt, float eps, void *stream);
+
+/*
+ * qknorm_rotary_backward -- gradients of qknorm_rotary.
+ *
+ * With g the output's gradient turned back, inv the row's factor, d its width:
+ *   dx = inv * (w g - x * inv^2 * sum(w g x) / d),   dw = sum over rows of g x inv
+ * rotary_dim == 0: gradients of QK-Norm alone (qknorm_fused's, any n_seg).
+ *
+ * dq_out [T][dq], dk_out [T][dk]  gradients of the outputs, pitches ldgq, ldgk
+ * q, k, wq, wk                    the forward call's inputs
+ * dq_in, dk_in                    results in `act`, pitches lddq, lddk; they
+ *                                 must not overlap any input
+ * dwq [dq], dwk [dk]              results, fp32, always written (zeros when T == 0)
+ * workspace    at least qknorm_rotary_backward_workspace_bytes(T, dq, dk)
+ *              bytes of device scratch, 16-byte aligned, or NULL to allocate
+ *              it stream-ordered inside the call
+ * Sums are fp32 in a fixed order: repeated calls give the same bits.
+ */
+QKN_API qkn_status qknorm_rotary_backward(const void *dq_out, const void *dk_out,
+                                          const void *q, const void *k, const void *wq, const void *wk,
+                                          void *dq_in, void *dk_in, float *dwq, float *dwk,
+                                          int64_t T, int64_t dq, int64_t dk,
+                                          int64_t ldgq, int64_t ldgk, int64_t ldq, int64_t ldk,
+                                          int64_t lddq, int64_t lddk,
+                                          int64_t head_dim, const void *positions, int pos_bits,
+                                          const double *inv_freq, int64_t rotary_dim,
+                                          qkn_rotary_layout layout, float mscale,
+                                          qkn_dtype act, qkn_dtype wdt, float eps,
+                                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace qknorm_rotary_backward needs (0 for invalid sizes). */
+QKN_API size_t qknorm_rotary_backward_workspace_bytes(int64_t T, int64_t dq, int64_t dk);
+
+/*
  * qkn_check_device -- synchronises `stream`, then reads and clears the
  * current device's error word.  Returns QKN_ERR_TIMEOUT when a bounded
  * device-side wait of an earlier launch (the projection kernel's mbarrier

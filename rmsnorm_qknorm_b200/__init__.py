@@ -18,6 +18,9 @@ Entry points (same names as the C ABI):
   GEMM with the scaling in the epilogue.
 * :func:`rmsnorm_apply_partials` -- the apply step of tensor-parallel QK-Norm:
   normalise a shard from the gathered per-shard partial sums.
+* :func:`rotary_apply` -- rotary positions on query and key rows (and back).
+* :func:`qknorm_rotary`, :func:`qknorm_rotary_backward` -- QK-Norm and rotary
+  positions in one pass, and the gradients of both.
 * :func:`qkv_norm_proj` -- QKV projection + QKV-normalisation with the
   pre-attention RMSNorm eliminated (FlashNorm's scale-invariance identity).
 """
@@ -28,6 +31,8 @@ import os
 import threading
 
 import torch
+
+from .rotary import rotary_inv_freq
 
 __all__ = [
     "QKNormError",
@@ -43,6 +48,11 @@ __all__ = [
     "flashnorm_inv_rms",
     "rmsnorm_apply_partials",
     "qkv_norm_proj",
+    "rotary_inv_freq",
+    "rotary_apply",
+    "qknorm_rotary",
+    "qknorm_rotary_backward",
+    "qknorm_rotary_backward_workspace_bytes",
     "STATUS_NAMES",
     "QKN_MAX_SEG",
 ]
@@ -100,9 +110,16 @@ def load_library() -> ctypes.CDLL:
         lib.qkv_proj_qknorm_workspace_bytes.argtypes = [i64, i64, i64, i64]
         lib.qkv_proj_qknorm_workspace_bytes.restype = ctypes.c_size_t
         lib.flashnorm_inv_rms.argtypes = [p, p, i64, i64, f32, p]
+        lib.rotary_apply.argtypes = [p, p, p, p] + [i64] * 8 + [p, i32, p, i64, i32, f32, i32, i32, p]
+        lib.qknorm_rotary.argtypes = [p] * 6 + [i64] * 8 + [p, i32, p, i64, i32, f32, i32, i32, f32, p]
+        lib.qknorm_rotary_backward.argtypes = ([p] * 10 + [i64] * 10 + [p, i32, p, i64, i32, f32, i32, i32, f32,
+                                                                      p, ctypes.c_size_t, p])
+        lib.qknorm_rotary_backward_workspace_bytes.argtypes = [i64, i64, i64]
+        lib.qknorm_rotary_backward_workspace_bytes.restype = ctypes.c_size_t
         lib.qkn_check_device.argtypes = [p]
         for f in ("qknorm_fused", "qknorm_fused_host", "qkv_proj_qknorm", "rmsnorm_partial_stats", "flashnorm_fold_weights",
-                  "flashnorm_proj", "flashnorm_inv_rms", "rmsnorm_apply_partials", "qkv_norm_proj", "qkn_check_device"):
+                  "flashnorm_proj", "flashnorm_inv_rms", "rmsnorm_apply_partials", "qkv_norm_proj", "rotary_apply", "qknorm_rotary",
+                  "qknorm_rotary_backward", "qkn_check_device"):
             getattr(lib, f).restype = ctypes.c_int
         lib.qkn_last_error.restype = ctypes.c_char_p
         lib.qkn_last_error.argtypes = []
@@ -555,3 +572,206 @@ def qkv_proj_qknorm(x: torch.Tensor, W_folded: torch.Tensor, nq: int, nk: int, n
             ws_ptr, ws_bytes, _stream(stream))
     _check("qkv_proj_qknorm", st)
     return out
+
+
+class _AllocOn:
+    """Allocations made for a call on `stream` come from that stream's memory pool.
+
+    A tensor from the current stream's pool may still be in use by work queued
+    there, which `stream` does not wait for.
+    """
+
+    __slots__ = ("ctx",)
+
+    def __init__(self, stream, dev: torch.device):
+        self.ctx = None
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                handle = int(stream)
+                stream = torch.cuda.ExternalStream(handle, dev) if handle else torch.cuda.default_stream(dev)
+            self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _rotary_args(positions, inv_freq, head_dim: int, layout: str, T: int, optional: bool):
+    """(head_dim, positions pointer, pos_bits, inv_freq pointer, rotary_dim, layout code) of a call."""
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout must be 'half' or 'interleaved', not {layout!r}")
+    if inv_freq is None:
+        if not optional:
+            raise ValueError("inv_freq is required")
+        return 0, None, 64, None, 0, LAYOUTS[layout]
+    _cuda(inv_freq, "inv_freq")
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous 1-D float64 tensor")
+    if positions is None:
+        raise ValueError("positions is required with inv_freq")
+    _vec(positions, "positions", T)
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be int32 or int64")
+    return (int(head_dim), positions.data_ptr(), 64 if positions.dtype == torch.int64 else 32, inv_freq.data_ptr(),
+            2 * inv_freq.shape[0], LAYOUTS[layout])
+
+
+def _rows_like(t: torch.Tensor, name: str, q: torch.Tensor):
+    rows, d, ld = _rows(t, name)
+    if rows != q.shape[0] or t.dtype != q.dtype:
+        raise ValueError(f"{name} must have q's row count and dtype")
+    return d, ld
+
+
+def _pair_weights(wq, wk, dq: int, dk: int, has_k: bool) -> int:
+    _vec(wq, "wq", dq)
+    if has_k:
+        if wk is None:
+            raise ValueError("wk is required with k")
+        _vec(wk, "wk", dk)
+        if wk.dtype != wq.dtype:
+            raise ValueError("wk must have wq's dtype")
+    return _dtype_code(wq.dtype)
+
+
+def _row_outputs(q, k, q_out, k_out, dk: int, inplace: bool, stream):
+    """Output tensors of a call on q and k, their pointers (None in place) and pitches."""
+    if inplace:
+        if q_out is not None or k_out is not None:
+            raise ValueError("inplace=True takes no q_out or k_out")
+        return q, k, None, None, 0, 0
+    T, dq = q.shape
+    with _AllocOn(stream, q.device):
+        if q_out is None:
+            q_out = torch.empty((T, dq), dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty((T, dk), dtype=q.dtype, device=q.device)
+    _, _, ldq_o = _rows(_out2d(q_out, "q_out", T, dq, q.dtype), "q_out")
+    if k is None:
+        return q_out, None, q_out.data_ptr(), None, ldq_o, 0
+    _, _, ldk_o = _rows(_out2d(k_out, "k_out", T, dk, q.dtype), "k_out")
+    return q_out, k_out, q_out.data_ptr(), k_out.data_ptr(), ldq_o, ldk_o
+
+
+def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
+                 head_dim: int, *, layout: str = "half", mscale: float = 1.0, inverse: bool = False,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, inplace: bool = False,
+                 stream=None):
+    """Rotary positions on q [T, dq] and k [T, dk] (k may be None), one launch for both.
+
+    Each head of ``head_dim`` elements has its first ``2 * len(inv_freq)``
+    turned by ``positions[t] * inv_freq`` (``positions`` int32 or int64 [T],
+    ``inv_freq`` float64, see :func:`rotary_inv_freq`), the rest copied.
+    ``layout`` pairs element i with i + r/2 ("half") or 2i with 2i + 1
+    ("interleaved").  ``inverse=True`` turns back, which is the call's own
+    gradient.  Returns ``(q_out, k_out)``; pitches, outputs and ``inplace`` as
+    in :func:`qknorm_fused`.
+    """
+    T, dq, ldq = _rows(q, "q")
+    act = _dtype_code(q.dtype)
+    dk, ldk = _rows_like(k, "k", q) if k is not None else (0, 0)
+    D, pos, bits, freq, r, lay = _rotary_args(positions, inv_freq, head_dim, layout, T, False)
+    q_out, k_out, qp, kp, ldq_o, ldk_o = _row_outputs(q, k, q_out, k_out, dk, inplace, stream)
+    dev = _device(q, k=k, positions=positions, inv_freq=inv_freq, q_out=q_out, k_out=k_out)
+    with _On(dev):
+        st = load_library().rotary_apply(
+            q.data_ptr(), k.data_ptr() if k is not None else None, qp, kp, T, dq, dk, ldq, ldk, ldq_o, ldk_o, D, pos,
+            bits, freq, r, lay, float(mscale), int(bool(inverse)), act, _stream(stream))
+    _check("rotary_apply", st)
+    return q_out, k_out
+
+
+def qknorm_rotary(q: torch.Tensor, k: torch.Tensor | None, wq: torch.Tensor, wk: torch.Tensor | None,
+                  positions: torch.Tensor | None, inv_freq: torch.Tensor | None, head_dim: int, eps: float = 1e-6, *,
+                  layout: str = "half", mscale: float = 1.0, q_out: torch.Tensor | None = None,
+                  k_out: torch.Tensor | None = None, inplace: bool = False, stream=None):
+    """QK-Norm of the full rows of q and k, then rotary positions, in one pass over them.
+
+    The statistic is :func:`qknorm_fused`'s with ``n_seg=1``; the normalised
+    rows are not rounded before they are turned.  ``inv_freq=None`` leaves the
+    rotation out.  Returns ``(q_out, k_out)``; arguments as in
+    :func:`qknorm_fused` and :func:`rotary_apply`.
+    """
+    T, dq, ldq = _rows(q, "q")
+    act = _dtype_code(q.dtype)
+    dk, ldk = _rows_like(k, "k", q) if k is not None else (0, 0)
+    wdt = _pair_weights(wq, wk, dq, dk, k is not None)
+    D, pos, bits, freq, r, lay = _rotary_args(positions, inv_freq, head_dim, layout, T, True)
+    q_out, k_out, qp, kp, ldq_o, ldk_o = _row_outputs(q, k, q_out, k_out, dk, inplace, stream)
+    dev = _device(q, k=k, wq=wq, wk=wk if k is not None else None, positions=positions if r else None,
+                  inv_freq=inv_freq, q_out=q_out, k_out=k_out)
+    with _On(dev):
+        st = load_library().qknorm_rotary(
+            q.data_ptr(), k.data_ptr() if k is not None else None, wq.data_ptr(),
+            wk.data_ptr() if k is not None else None, qp, kp, T, dq, dk, ldq, ldk, ldq_o, ldk_o, D, pos, bits, freq,
+            r, lay, float(mscale), act, wdt, float(eps), _stream(stream))
+    _check("qknorm_rotary", st)
+    return q_out, k_out
+
+
+def qknorm_rotary_backward_workspace_bytes(T: int, dq: int, dk: int) -> int:
+    """Device scratch qknorm_rotary_backward needs for these sizes (bytes)."""
+    return int(load_library().qknorm_rotary_backward_workspace_bytes(T, dq, dk))
+
+
+def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.Tensor, k: torch.Tensor | None,
+                           wq: torch.Tensor, wk: torch.Tensor | None, positions: torch.Tensor | None,
+                           inv_freq: torch.Tensor | None, head_dim: int, eps: float = 1e-6, *, layout: str = "half",
+                           mscale: float = 1.0, dq_out: torch.Tensor | None = None,
+                           dk_out: torch.Tensor | None = None, dwq_out: torch.Tensor | None = None,
+                           dwk_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of :func:`qknorm_rotary` (of :func:`qknorm_fused` with ``inv_freq=None``).
+
+    ``gq``, ``gk`` are the gradients of its two outputs, the other arguments
+    those it was called with.  Returns ``(dq, dk, dwq, dwk)``: dq and dk in
+    q's dtype, dwq and dwk in float32 (None for k when k is None).  The
+    results must not overlap the inputs.  ``workspace`` (uint8 CUDA tensor of
+    at least ``qknorm_rotary_backward_workspace_bytes``) avoids an allocation
+    inside the call.
+    """
+    T, dq, ldq = _rows(q, "q")
+    act = _dtype_code(q.dtype)
+    has_k = k is not None
+    if has_k != (gk is not None):
+        raise ValueError("gk is given with k, and only with k")
+    dgq, ldgq = _rows_like(gq, "gq", q)
+    dk, ldk = _rows_like(k, "k", q) if has_k else (0, 0)
+    dgk, ldgk = _rows_like(gk, "gk", q) if has_k else (0, 0)
+    if dgq != dq or dgk != dk:
+        raise ValueError("gq and gk must have the widths of q and k")
+    wdt = _pair_weights(wq, wk, dq, dk, has_k)
+    D, pos, bits, freq, r, lay = _rotary_args(positions, inv_freq, head_dim, layout, T, True)
+    dq_t, dk_t, qp, kp, ld_dq, ld_dk = _row_outputs(q, k, dq_out, dk_out, dk, False, stream)
+    with _AllocOn(stream, q.device):
+        if dwq_out is None:
+            dwq_out = torch.empty(dq, dtype=torch.float32, device=q.device)
+        if has_k and dwk_out is None:
+            dwk_out = torch.empty(dk, dtype=torch.float32, device=q.device)
+    for name, t, n in (("dwq_out", dwq_out, dq), ("dwk_out", dwk_out if has_k else None, dk)):
+        if t is not None:
+            _vec(t, name, n)
+            if t.dtype != torch.float32:
+                raise ValueError(f"{name} must be fp32")
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        _cuda(workspace, "workspace")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    dev = _device(q, gq=gq, k=k, gk=gk, wq=wq, wk=wk if has_k else None, positions=positions if r else None,
+                  inv_freq=inv_freq, dq_out=dq_t, dk_out=dk_t, dwq_out=dwq_out, dwk_out=dwk_out if has_k else None,
+                  workspace=workspace)
+    with _On(dev):
+        st = load_library().qknorm_rotary_backward(
+            gq.data_ptr(), gk.data_ptr() if has_k else None, q.data_ptr(), k.data_ptr() if has_k else None,
+            wq.data_ptr(), wk.data_ptr() if has_k else None, qp, kp, dwq_out.data_ptr(),
+            dwk_out.data_ptr() if has_k else None, T, dq, dk, ldgq, ldgk, ldq, ldk, ld_dq, ld_dk, D, pos, bits, freq,
+            r, lay, float(mscale), act, wdt, float(eps), ws_ptr, ws_bytes, _stream(stream))
+    _check("qknorm_rotary_backward", st)
+    return dq_t, dk_t, dwq_out, (dwk_out if has_k else None)
