@@ -760,10 +760,12 @@ def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.T
             _vec(t, name, n)
             if t.dtype != torch.float32:
                 raise ValueError(f"{name} must be fp32")
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        _cuda(workspace, "workspace")
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace is None:
+        with _On(q.device):  # the size goes by the device's number of SMs
+            need = qknorm_rotary_backward_workspace_bytes(T, dq, dk)
+        with _AllocOn(stream, q.device):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _cuda(workspace, "workspace")
     dev = _device(q, gq=gq, k=k, gk=gk, wq=wq, wk=wk if has_k else None, positions=positions if r else None,
                   inv_freq=inv_freq, dq_out=dq_t, dk_out=dk_t, dwq_out=dwq_out, dwk_out=dwk_out if has_k else None,
                   workspace=workspace)
@@ -772,6 +774,7 @@ def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.T
             gq.data_ptr(), gk.data_ptr() if has_k else None, q.data_ptr(), k.data_ptr() if has_k else None,
             wq.data_ptr(), wk.data_ptr() if has_k else None, qp, kp, dwq_out.data_ptr(),
             dwk_out.data_ptr() if has_k else None, T, dq, dk, ldgq, ldgk, ldq, ldk, ld_dq, ld_dk, D, pos, bits, freq,
-            r, lay, float(mscale), act, wdt, float(eps), ws_ptr, ws_bytes, _stream(stream))
+            r, lay, float(mscale), act, wdt, float(eps), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(stream))
     _check("qknorm_rotary_backward", st)
     return dq_t, dk_t, dwq_out, (dwk_out if has_k else None)

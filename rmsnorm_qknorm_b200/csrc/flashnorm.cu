@@ -753,12 +753,13 @@ extern "C" QKN_API qkn_status qkn_check_device(void *stream) {
         const int zero = 0;
         cudaMemcpyToSymbol(g_device_error, &zero, sizeof zero);
     }
-    int norm_flag = 0, qkv_flag = 0;
+    int norm_flag = 0, qkv_flag = 0, rotary_flag = 0;
     if (qkn_status st = read_norm_error(&norm_flag)) return st;
     if (qkn_status st = read_qkv_error(&qkv_flag)) return st;
-    if (flag != 0 || norm_flag != 0 || qkv_flag != 0)
-        return fail(QKN_ERR_TIMEOUT, "a bounded device-side wait gave up (projection %d, norm %d, fused QKV %d)", flag,
-                    norm_flag, qkv_flag);
+    if (qkn_status st = read_rotary_error(&rotary_flag)) return st;
+    if (flag != 0 || norm_flag != 0 || qkv_flag != 0 || rotary_flag != 0)
+        return fail(QKN_ERR_TIMEOUT, "a bounded device-side wait gave up (projection %d, norm %d, fused QKV %d, rotary %d)",
+                    flag, norm_flag, qkv_flag, rotary_flag);
     return QKN_OK;
 }
 

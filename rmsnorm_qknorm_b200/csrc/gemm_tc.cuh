@@ -93,4 +93,7 @@ qkn_status launch_inv_rms(const void *x, float *inv, int64_t M, int64_t K, float
 // Reads (and clears) the device error word of the fused QKV + QK-Norm kernel.
 qkn_status read_qkv_error(int *flag);
 
+// Reads (and clears) the device error word of the rotary unit kernel.
+qkn_status read_rotary_error(int *flag);
+
 }  // namespace qkn

@@ -260,9 +260,23 @@ __global__ void __launch_bounds__(kBlock) dw_reduce_kernel(const float *__restri
     }
 }
 
+}  // namespace rot
+}  // namespace qkn
+
+#include "rotary_rows.cuh"
+
+namespace qkn {
+namespace rot {
+
 // ---------------------------------------------------------------- host side
 
 constexpr int kScalarSlices = 64;
+
+qkn_status launch_dw_reduce(const Args &a, int slices, cudaStream_t s) {
+    const int dq = a.job[0].d, dk = a.njobs > 1 ? a.job[1].d : 0;
+    dw_reduce_kernel<<<(unsigned)((dq + dk + 31) / 32), kBlock, 0, s>>>(a.part, a.job[0].dw, a.job[1].dw, dq, dk, slices);
+    return check_launch("dw_reduce_kernel launch");
+}
 
 template <typename TA, typename TW, int MODE>
 qkn_status launch_scalar(Args &a, cudaStream_t s) {
@@ -276,15 +290,18 @@ qkn_status launch_scalar(Args &a, cudaStream_t s) {
         const dim3 grid((unsigned)((widest + kBlock - 1) / kBlock), (unsigned)a.slices, (unsigned)a.njobs);
         rotary_scalar_dw_kernel<TA, TW><<<grid, kBlock, 0, s>>>(a);
         if (qkn_status st = check_launch("rotary_scalar_dw_kernel launch")) return st;
-        dw_reduce_kernel<<<(unsigned)((dq + dk + 31) / 32), kBlock, 0, s>>>(a.part, a.job[0].dw, a.job[1].dw, dq, dk,
-                                                                           a.slices);
-        return check_launch("dw_reduce_kernel launch");
+        return launch_dw_reduce(a, a.slices, s);
     }
     return QKN_OK;
 }
 
 template <typename TA, typename TW, int MODE>
 qkn_status launch(Args &a, cudaStream_t s) {
+    bool taken = false;
+    int grid = 0;
+    const qkn_status st = unit::launch<TA, TW, MODE>(a, &taken, &grid, s);
+    if (st != QKN_OK) return st;
+    if (taken) return MODE == kNormBack ? launch_dw_reduce(a, grid, s) : QKN_OK;
     return launch_scalar<TA, TW, MODE>(a, s);
 }
 
@@ -417,9 +434,12 @@ extern "C" QKN_API qkn_status qknorm_rotary(const void *q, const void *k, const 
 
 extern "C" QKN_API size_t qknorm_rotary_backward_workspace_bytes(int64_t T, int64_t dq, int64_t dk) {
     if (T < 0 || dq < 1 || dk < 0 || dq > 0x3fffffffLL || dk > 0x3fffffffLL || T > (1LL << 40)) return 0;
-    // element-wise kernels: row factors of both tensors, then the slices' partial sums
+    // row factors of both tensors (element-wise kernels), then rows of partial sums: one per
+    // slice of the element-wise kernel or per block of the unit kernel
     const size_t inv = ((size_t)T * 2 * 4 + 255) / 256 * 256;
-    return inv + (size_t)rot::kScalarSlices * (size_t)(dq + dk) * 4;
+    const size_t blocks = (size_t)rot::unit::kMaxCtas * (size_t)sm_count();
+    const size_t parts = blocks > (size_t)rot::kScalarSlices ? blocks : (size_t)rot::kScalarSlices;
+    return inv + ((size_t)T < parts ? (size_t)T : parts) * (size_t)(dq + dk) * 4;
 }
 
 extern "C" QKN_API qkn_status qknorm_rotary_backward(
