@@ -6,28 +6,32 @@
 //
 // The work is all HBM: every row is read once and written once (gradients:
 // x and dy read, dx written).  A token's rows (q and k together) are handled
-// by a group of G warps; a block holds NG groups that never wait for one
+// by a group of G + 1 warps; a block holds NG groups that never wait for one
 // another.  Each group owns a ring of stages in shared memory, one token per
-// stage, filled by 1-D bulk copies that run while earlier tokens are
-// computed.
+// stage.  The group's last warp is its producer: it fills a stage with 1-D
+// bulk copies of the token's rows and, while they fly, forms the cos and sin
+// of the token's angles into the stage's table, up to `stages` tokens ahead
+// of the G consumer warps.  (With the table formed by the consumers between
+// their loads and the row's barrier the fp64 angle and sincospif sat on every
+// token's critical path.)
 //
-// A thread owns the same columns of every token: UPT "units" of two 16-byte
-// chunks, chunk j and chunk j + r / 2E of a head (E elements per chunk).  In
-// the half layout the two chunks hold the two sides of E pairs; in the
-// interleaved layout each holds E / 2 whole pairs.  Either way a unit needs
-// the cos and sin of two runs of E / 2 frequencies, which the group's table
+// A consumer thread owns the same columns of every token: UPT "units" of two
+// 16-byte chunks, chunk j and chunk j + r / 2E of a head (E elements per
+// chunk).  In the half layout the two chunks hold the two sides of E pairs;
+// in the interleaved layout each holds E / 2 whole pairs.  Either way a unit
+// needs the cos and sin of two runs of E / 2 frequencies, which the table
 // keeps at positions j and j + r / 2E (filled in the order the layout asks
-// for), so the arithmetic below is the same for both and neighbouring threads
-// read neighbouring 16-byte words.  Chunks behind the rotated part form units
-// of their own, copied (or only normalised).  Fixed columns keep the weights,
-// and the weights' gradients, in registers over all tokens.
+// for), so neighbouring threads read neighbouring 16-byte words.  Chunks
+// behind the rotated part form units of their own, copied (or only
+// normalised).  Fixed columns keep the weights' gradients in registers over
+// all tokens; the weights are read from a copy in shared memory.
 //
-// One barrier per token: before it, threads read their chunks, add up squares
-// and park the warp's sums, and fill the table of the NEXT token; after it
-// the stage is free (every thread holds its chunks in registers) and is
-// refilled, the row's factor is formed and the results are stored.  Sums are
-// double-buffered and tables triple-buffered by token, which one barrier per
-// token makes safe.
+// With the norm, consumers meet at one barrier per token: before it they read
+// their chunks, add up squares, multiply by the weights and park their warp's
+// sums; after it they form the row's factor, turn, scale and store.  q and k
+// have warps of their own (a group of one warp adds up both).  The sums are
+// double-buffered by token, which one barrier per token makes safe.  The two
+// halves of a packed fp32x2 operation round like scalar ones.
 #pragma once
 
 namespace qkn {
@@ -61,15 +65,20 @@ struct Params {
     const double *freq;
     float mscale, sign, eps;
     float *part;             // gradients: [gridDim.x][dq + dk]
-    int warps, groups;       // warps per group, groups per block
+    int warps, groups;       // consumer warps per group, groups per block
+    int warps0;              // consumer warps of job 0 (== warps when one warp serves both jobs)
     int stages, stage_bytes, x_bytes;
+    int w_bytes;             // the block's copy of the weights, in front of the rings
     uint64_t wait_ns;
 };
 
-inline __host__ __device__ int table_bytes(int r) { return 3 * r * 4; }          // cos and sin of 3 tokens
-inline __host__ __device__ int red_bytes(int warps) { return 2 * warps * 16; }   // 2 x 4 sums per warp
-inline __host__ __device__ int group_fixed(int r, int warps, int stages) {
-    return (table_bytes(r) + 15) / 16 * 16 + red_bytes(warps) + (stages + 1) / 2 * 16;
+constexpr int kMaxWarps = 15;  // consumer warps per group
+constexpr int kSlots = 16;     // sums per tensor and token
+
+inline __host__ __device__ int table_bytes(int r) { return (r * 4 + 15) / 16 * 16; }  // cos and sin of a token
+// per group: tables, 2 tokens x (sum x^2, sum w g x) x kSlots sums, full and empty barriers
+inline __host__ __device__ int group_fixed(int r, int stages) {
+    return stages * table_bytes(r) + 4 * kSlots * 4 + stages * 16;
 }
 
 __device__ __forceinline__ Rows pick(const Params &a, int which) {
@@ -93,7 +102,7 @@ __device__ __forceinline__ Rows pick(const Params &a, int which) {
     return J;
 }
 
-// Barrier of a group, true on every thread when any of them failed.
+// Barrier of a group's consumers, true on every thread when any of them failed.
 __device__ __forceinline__ bool group_sync_or(bool failed, int group, int warps) {
     if (warps == 1) {
         const bool any = __any_sync(0xffffffffu, failed);
@@ -113,330 +122,403 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
-// H = E / 2 consecutive floats of the table.
-template <int H>
-__device__ __forceinline__ void lds_run(uint32_t addr, float (&f)[H]) {
-    if constexpr (H == 4)
-        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(addr));
-    else
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "r"(addr));
-}
-
-// The two chunks of a unit, turned.
-template <int E, bool HALF>
-__device__ __forceinline__ void turn(float (&a)[E], float (&b)[E], uint32_t cos_addr, uint32_t run, uint32_t sin_off) {
-    constexpr int H = E / 2;
-    float c0[H], s0[H], c1[H], s1[H];
-    lds_run<H>(cos_addr, c0);
-    lds_run<H>(cos_addr + run, c1);
-    lds_run<H>(cos_addr + sin_off, s0);
-    lds_run<H>(cos_addr + sin_off + run, s1);
-    if constexpr (HALF) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float c = e < H ? c0[e % H] : c1[e % H], s = e < H ? s0[e % H] : s1[e % H];
-            const float x = a[e], y = b[e];
-            a[e] = x * c - y * s;
-            b[e] = y * c + x * s;
-        }
+// A 16-byte chunk as E / 2 pairs of fp32.
+template <typename TA, int H> __device__ __forceinline__ void unpack2(const uint4 &v, float2 (&f)[H]) {
+    if constexpr (sizeof(TA) == 4) {
+        f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
     } else {
+        f[0] = make_float2(bf16lo(v.x), bf16hi(v.x));
+        f[1] = make_float2(bf16lo(v.y), bf16hi(v.y));
+        f[2] = make_float2(bf16lo(v.z), bf16hi(v.z));
+        f[3] = make_float2(bf16lo(v.w), bf16hi(v.w));
+    }
+}
+template <typename TA, int H> __device__ __forceinline__ uint4 pack2(const float2 (&f)[H]) {
+    if constexpr (sizeof(TA) == 4)
+        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+    else
+        return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                          pack_bf16x2(f[3].x, f[3].y));
+}
+
+// H = E / 2 consecutive floats of the table, as pairs.
+template <int H>
+__device__ __forceinline__ void lds_run(uint32_t addr, float2 (&f)[H / 2]) {
+    if constexpr (H == 4)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y) : "r"(addr));
+    else
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0].x), "=f"(f[0].y) : "r"(addr));
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// The two chunks of a unit, turned and (SCALE) multiplied by inv.
+template <int H, bool HALF, bool SCALE>
+__device__ __forceinline__ void turn(float2 (&a)[H], float2 (&b)[H], uint32_t cos_addr, uint32_t run, uint32_t sin_off,
+                                     float inv) {
 #pragma unroll
-        for (int e = 0; e < H; ++e) {
-            const float x = a[2 * e], y = a[2 * e + 1], z = b[2 * e], w = b[2 * e + 1];
-            a[2 * e] = x * c0[e] - y * s0[e];
-            a[2 * e + 1] = y * c0[e] + x * s0[e];
-            b[2 * e] = z * c1[e] - w * s1[e];
-            b[2 * e + 1] = w * c1[e] + z * s1[e];
+    for (int q = 0; q < 2; ++q) {
+        float2 c[H / 2], s[H / 2];
+        lds_run<H>(cos_addr + (q ? run : 0u), c);
+        lds_run<H>(cos_addr + sin_off + (q ? run : 0u), s);
+        if constexpr (HALF) {
+#pragma unroll
+            for (int p = 0; p < H / 2; ++p) {
+                const int i = q * (H / 2) + p;
+                const float2 x = a[i], y = b[i];
+                const float2 xc = __fmul2_rn(x, c[p]), ys = __fmul2_rn(y, s[p]), yc = __fmul2_rn(y, c[p]);
+                if constexpr (SCALE) {
+                    a[i] = __ffma2_rn(ys, both(-inv), __fmul2_rn(xc, both(inv)));
+                    b[i] = __fmul2_rn(__ffma2_rn(x, s[p], yc), both(inv));
+                } else {
+                    a[i] = __ffma2_rn(ys, both(-1.f), xc);
+                    b[i] = __ffma2_rn(x, s[p], yc);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                const float ce = (e & 1) ? c[e >> 1].y : c[e >> 1].x, se = (e & 1) ? s[e >> 1].y : s[e >> 1].x;
+                const float2 v = q ? b[e] : a[e];
+                float2 t = make_float2(v.x * ce - v.y * se, v.y * ce + v.x * se);
+                if constexpr (SCALE) t = __fmul2_rn(t, both(inv));
+                if (q) b[e] = t;
+                else a[e] = t;
+            }
         }
     }
 }
 
-// The weights of a chunk, as they are stored.
-template <typename TW, int E> struct RawWeights {
-    static constexpr int N = E * (int)sizeof(TW) / 4;
-    uint32_t v[N];
-    __device__ __forceinline__ void load(const void *w, int element) {
-        const uint32_t *p = reinterpret_cast<const uint32_t *>(static_cast<const TW *>(w) + element);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __ldg(p + i);
+// The weights of a chunk from shared memory, as pairs.
+template <typename TW, int H>
+__device__ __forceinline__ void lds_weights(uint32_t addr, float2 (&f)[H]) {
+    if constexpr (sizeof(TW) * 2 * H == 32) {  // fp32 weights of 8 elements
+        const uint4 a = lds128(addr), b = lds128(addr + 16);
+        f[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+        f[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+        f[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+        f[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+    } else if constexpr (sizeof(TW) * 2 * H == 16) {
+        unpack2<TW, H>(lds128(addr), f);
+    } else {  // bf16 weights of 4 elements
+        uint2 v;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+        f[0] = make_float2(bf16lo(v.x), bf16hi(v.x));
+        f[1] = make_float2(bf16lo(v.y), bf16hi(v.y));
     }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = 0u;
-    }
-    __device__ __forceinline__ float get(int e) const {
-        if constexpr (sizeof(TW) == 4) return __uint_as_float(v[e]);
-        else return (e & 1) ? bf16hi(v[e >> 1]) : bf16lo(v[e >> 1]);
-    }
-};
+}
 
-template <typename TA, typename TW, int MODE, int UPT, bool HALF>
-__global__ void __launch_bounds__(kMaxThreads, (MODE == kNormBack || UPT == 4) ? 1 : 2)
+__device__ __forceinline__ float warp_sum(float v) {
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// WIDE: groups of up to 15 consumer warps; otherwise up to 10, two blocks per SM where the registers allow.
+template <bool WIDE> constexpr int max_threads() { return WIDE ? 32 * (kMaxWarps + 1) : 32 * 11; }
+#ifndef ROT_MINB
+#define ROT_MINB 2
+#endif
+#ifndef ROT_MINB_BACK
+#define ROT_MINB_BACK 1
+#endif
+
+template <typename TA, typename TW, int MODE, int UPT, bool HALF, bool WIDE>
+__global__ void __launch_bounds__(max_threads<WIDE>(), WIDE ? 1 : MODE == kNormBack ? ROT_MINB_BACK : ROT_MINB)
 rotary_unit_kernel(const Params a) {
     constexpr int E = Chunk<TA>::E, H = E / 2;
     constexpr bool NORM = MODE != kRotate, BACK = MODE == kNormBack;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int threads = a.warps * 32;
-    const int group = threadIdx.x / threads, gt = threadIdx.x - group * threads;  // thread within its group
+    const int gthreads = (a.warps + 1) * 32;
+    const int group = threadIdx.x / gthreads, gt = threadIdx.x - group * gthreads;  // thread within its group
     const int lane = threadIdx.x & 31, gw = gt >> 5;
-    const int fixed = group_fixed(a.r, a.warps, a.stages);
-    uint8_t *ring_p = smem + (size_t)group * a.stages * a.stage_bytes;
-    uint8_t *fix_p = smem + (size_t)a.groups * a.stages * a.stage_bytes + (size_t)group * fixed;
-    const uint32_t ring = smem_u32(ring_p);
-    float *table = reinterpret_cast<float *>(fix_p);
-    float4 *red = reinterpret_cast<float4 *>(fix_p + (table_bytes(a.r) + 15) / 16 * 16);
-    const uint32_t bars = smem_u32(red + 2 * a.warps);
-    const uint32_t table_s = smem_u32(table);
-    const uint32_t sin_off = (uint32_t)a.r * 2u, run = (uint32_t)a.rot_units * H * 4u;  // bytes
-
-    if (gt == 0) {
-        for (int s = 0; s < a.stages; ++s) mbar_init(bars + 8u * s, 1);
-        mbar_init_fence();
-    }
-
-    // this thread's units
-    int off_a[UPT], off_b[UPT], tab[UPT];  // stage offsets of the chunks (-1: none), table offset (-1: not turned)
-    uint32_t is_k = 0;
-#pragma unroll
-    for (int i = 0; i < UPT; ++i) {
-        int u = gt + i * threads;
-        off_a[i] = off_b[i] = tab[i] = -1;
-        const int which = u >= a.job[0].nunits ? 1 : 0;
-        if (which) {
-            u -= a.job[0].nunits;
-            is_k |= 1u << i;
-        }
-        if (which >= a.njobs || u >= (which ? a.job[1].nunits : a.job[0].nunits)) continue;
-        const Rows J = pick(a, which);
-        const int h = u / J.units_per_head, j = u - h * J.units_per_head;
-        const int first = h * J.head_chunks;
-        if (j < a.rot_units) {
-            off_a[i] = J.row_off + (first + j) * 16;
-            off_b[i] = off_a[i] + a.rot_units * 16;
-            tab[i] = j * H * 4;
-        } else {
-            const int t = j - a.rot_units;
-            off_a[i] = J.row_off + (first + 2 * a.rot_units + t) * 16;
-            if (t + J.tail_units < J.tail_chunks) off_b[i] = off_a[i] + J.tail_units * 16;
-        }
-    }
-
-    // the previous kernel on the stream has finished before any memory is touched
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
+    uint8_t *rings = smem + a.w_bytes;
+    uint8_t *fix_p = rings + (size_t)a.groups * a.stages * a.stage_bytes + (size_t)group * group_fixed(a.r, a.stages);
+    const uint32_t ring = smem_u32(rings + (size_t)group * a.stages * a.stage_bytes);
+    const int tbytes = table_bytes(a.r);
+    float *red = reinterpret_cast<float *>(fix_p + (size_t)a.stages * tbytes);
+    const uint32_t full = smem_u32(red + 4 * kSlots), empty = full + 8u * a.stages;
     const int64_t step = (int64_t)gridDim.x * a.groups;
     const int64_t first_token = (int64_t)blockIdx.x * a.groups + group;
-    __syncthreads();  // barriers initialised
 
-    auto issue = [&](int64_t n, int stage) {
-        const uint32_t bar = bars + 8u * stage, dst = ring + (uint32_t)(stage * a.stage_bytes);
-        mbar_arrive_expect_tx(bar, (uint32_t)a.stage_bytes);
-        bulk_g2s(dst, a.job[0].x + n * a.job[0].ldx, a.job[0].row_bytes, bar);
-        if (BACK) bulk_g2s(dst + a.x_bytes, a.job[0].g + n * a.job[0].ldg, a.job[0].row_bytes, bar);
-        if (a.njobs > 1) {
-            bulk_g2s(dst + a.job[1].row_off, a.job[1].x + n * a.job[1].ldx, a.job[1].row_bytes, bar);
-            if (BACK)
-                bulk_g2s(dst + a.x_bytes + a.job[1].row_off, a.job[1].g + n * a.job[1].ldg, a.job[1].row_bytes, bar);
+    if (gt == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(full + 8u * s, 2);         // the producer's two arrivals and the copies' bytes
+            mbar_init(empty + 8u * s, a.warps);  // one per consumer warp
         }
-    };
-    int64_t issued = 0;  // stages filled so far (thread 0 of the group)
-    if (gt == 0)
-        for (int64_t n = first_token; issued < a.stages && n < a.T; n += step) issue(n, (int)issued), ++issued;
+        mbar_init_fence();
+    }
+    for (int i = gt; i < 4 * kSlots; i += gthreads) red[i] = 0.f;
+    // the previous kernel on the stream has finished before any global memory is touched
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (NORM) {  // weights word by word, at the element positions of a stage's rows
+        const int d0 = a.job[0].d, words = (int)sizeof(TW) * (d0 + a.job[1].d) / 4, words0 = (int)sizeof(TW) * d0 / 4;
+        for (int i = threadIdx.x; i < words; i += blockDim.x)
+            reinterpret_cast<uint32_t *>(smem)[i] = i < words0 ? __ldg(static_cast<const uint32_t *>(a.job[0].w) + i)
+                                                               : __ldg(static_cast<const uint32_t *>(a.job[1].w) + i - words0);
+    }
+    __syncthreads();
 
-    RawWeights<TW, E> wa[UPT], wb[UPT];
-    if constexpr (NORM) {
+    float2 da[UPT][H], db[UPT][H];  // gradients of the weights, over this group's tokens
+    int off_a[UPT], off_b[UPT], tab[UPT];  // stage offsets of a unit's chunks (-1: none), table offset (-1: not turned)
+    uint32_t is_k = 0;
+
+    if (gw == a.warps) {
+        // ---------------------------------------------------------------- producer warp
+        const int nf = a.r >> 1;
+        // frequency f sits in run f / H; the runs are placed in the layout's order
+        auto place = [&](int f) {
+            const int q = f / H;
+            return (HALF ? (q & 1) * a.rot_units + (q >> 1) : q) * H + f % H;
+        };
+        double turns[2];
+        int at[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            turns[i] = lane + 32 * i < nf ? __ldg(a.freq + lane + 32 * i) * kInvTwoPi : 0.0;
+            at[i] = place(lane + 32 * i);
+        }
+        auto pos_at = [&](int64_t n) -> int64_t {
+            if (a.r == 0 || n >= a.T) return 0;
+            return a.pos64 ? __ldg(static_cast<const long long *>(a.pos) + n)
+                           : (int64_t)__ldg(static_cast<const int *>(a.pos) + n);
+        };
+        int stage = 0;
+        uint32_t phase = 0, issued = 0;
+        int64_t p = pos_at(first_token);
+        for (int64_t n = first_token; n < a.T; n += step) {
+            bool ok = mbar_wait_fast(empty + 8u * stage, phase ^ 1u, &g_rotary_error, a.wait_ns);
+            if (__any_sync(0xffffffffu, !ok)) break;
+            const uint32_t bar = full + 8u * stage;
+            if (lane == 0) {
+                const uint32_t dst = ring + (uint32_t)(stage * a.stage_bytes);
+                mbar_arrive_expect_tx(bar, (uint32_t)a.stage_bytes);
+                bulk_g2s(dst, a.job[0].x + n * a.job[0].ldx, a.job[0].row_bytes, bar);
+                if (BACK) bulk_g2s(dst + a.x_bytes, a.job[0].g + n * a.job[0].ldg, a.job[0].row_bytes, bar);
+                if (a.njobs > 1) {
+                    bulk_g2s(dst + a.job[1].row_off, a.job[1].x + n * a.job[1].ldx, a.job[1].row_bytes, bar);
+                    if (BACK)
+                        bulk_g2s(dst + a.x_bytes + a.job[1].row_off, a.job[1].g + n * a.job[1].ldg, a.job[1].row_bytes,
+                                 bar);
+                }
+                issued |= 1u << stage;
+            }
+            const int64_t next = pos_at(n + step);
+            float *t = reinterpret_cast<float *>(fix_p + (size_t)stage * tbytes);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (lane + 32 * i < nf) cos_sin(p, turns[i], a.mscale, a.sign, t[at[i]], t[nf + at[i]]);
+            for (int f = lane + 64; f < nf; f += 32)
+                cos_sin(p, __ldg(a.freq + f) * kInvTwoPi, a.mscale, a.sign, t[place(f)], t[nf + place(f)]);
+            p = next;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+            if (++stage == a.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        // no copy may still be writing when the block exits: the last phase filled on every stage
+        // (on the normal path the consumers have waited for them all already)
+        if (lane == 0)
+            for (int s = 0; s < a.stages; ++s)
+                if (issued & (1u << s)) mbar_wait(full + 8u * s, s < stage ? phase : phase ^ 1u, &g_rotary_error, a.wait_ns);
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- consumer warps
+        const bool mixed = a.warps0 == a.warps && a.njobs > 1;  // one warp serves both jobs
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-            const bool k = (is_k >> i) & 1u;
-            const void *w = k ? a.job[1].w : a.job[0].w;
-            const int ro = k ? a.job[1].row_off : 0;
-            if (off_a[i] >= 0) wa[i].load(w, (off_a[i] - ro) / 16 * E);
-            else wa[i].clear();
-            if (off_b[i] >= 0) wb[i].load(w, (off_b[i] - ro) / 16 * E);
-            else wb[i].clear();
+            int which = mixed ? 0 : (gw >= a.warps0 ? 1 : 0);
+            const int jw = which ? a.warps - a.warps0 : a.warps0;
+            int u = gt - (which ? a.warps0 * 32 : 0) + i * jw * 32;
+            if (mixed && u >= a.job[0].nunits) {
+                u -= a.job[0].nunits;
+                which = 1;
+            }
+            off_a[i] = off_b[i] = tab[i] = -1;
+            if (which) is_k |= 1u << i;
+            if (u >= (which ? a.job[1].nunits : a.job[0].nunits)) continue;
+            const Rows J = pick(a, which);
+            const int h = u / J.units_per_head, j = u - h * J.units_per_head;
+            const int first = h * J.head_chunks;
+            if (j < a.rot_units) {
+                off_a[i] = J.row_off + (first + j) * 16;
+                off_b[i] = off_a[i] + a.rot_units * 16;
+                tab[i] = j * H * 4;
+            } else {
+                const int t = j - a.rot_units;
+                off_a[i] = J.row_off + (first + 2 * a.rot_units + t) * 16;
+                if (t + J.tail_units < J.tail_chunks) off_b[i] = off_a[i] + J.tail_units * 16;
+            }
         }
-    }
-    float da[UPT][E], db[UPT][E];  // gradients of the weights, over this group's tokens
-    if constexpr (BACK) {
+        const bool wk = !mixed && gw >= a.warps0;  // a warp of job 1 alone
+        const uint32_t w_s = smem_u32(smem);
+        // a chunk's weights: 16 bytes of elements are E weights
+        auto weights = [&](int off, float2 (&f)[H]) { lds_weights<TW, H>(w_s + (uint32_t)(off / 16 * (E * (int)sizeof(TW))), f); };
+        if constexpr (BACK) {
 #pragma unroll
-        for (int i = 0; i < UPT; ++i)
+            for (int i = 0; i < UPT; ++i)
 #pragma unroll
-            for (int e = 0; e < E; ++e) da[i][e] = db[i][e] = 0.f;
-    }
-
-    // cos and sin of a token: frequency f sits in run f / H, at the run's place in the layout's order
-    const int nf = a.r >> 1;
-    auto place = [&](int f) {
-        const int q = f / H;
-        return (HALF ? (q & 1) * a.rot_units + (q >> 1) : q) * H + f % H;
-    };
-    const double turns0 = gt < nf ? __ldg(a.freq + gt) * kInvTwoPi : 0.0;
-    const int place0 = place(gt);
-    auto fill = [&](int64_t p, int buf) {
-        float *t = table + buf * a.r;
-        if (gt < nf) cos_sin(p, turns0, a.mscale, a.sign, t[place0], t[nf + place0]);
-        for (int f = gt + threads; f < nf; f += threads)
-            cos_sin(p, __ldg(a.freq + f) * kInvTwoPi, a.mscale, a.sign, t[place(f)], t[nf + place(f)]);
-    };
-    auto pos_at = [&](int64_t n) -> int64_t {
-        if (a.r == 0 || n >= a.T) return 0;
-        return a.pos64 ? __ldg(static_cast<const long long *>(a.pos) + n) : (int64_t)__ldg(static_cast<const int *>(a.pos) + n);
-    };
-    int64_t next_pos = pos_at(first_token + step);
-    if (first_token < a.T) fill(pos_at(first_token), 0);
-    if (BACK || !NORM) group_sync_or(false, group, a.warps);  // the first table is read before the first token's barrier
-
-    int stage = 0, buf = 0, par = 0;
-    uint32_t phase = 0;
-    int64_t it = 0, n = first_token;
-    for (; n < a.T; n += step, ++it) {
-        const bool ok = mbar_wait_fast(bars + 8u * stage, phase, &g_rotary_error, a.wait_ns);
-        const uint32_t src = ring + (uint32_t)(stage * a.stage_bytes);
-        uint4 xa[UPT], xb[UPT];
-#pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-            xa[i] = off_a[i] >= 0 ? lds128(src + off_a[i]) : make_uint4(0u, 0u, 0u, 0u);
-            xb[i] = off_b[i] >= 0 ? lds128(src + off_b[i]) : make_uint4(0u, 0u, 0u, 0u);
+                for (int p = 0; p < H; ++p) da[i][p] = db[i][p] = make_float2(0.f, 0.f);
         }
-        float ga[UPT][E], gb[UPT][E];  // gradients turned back
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);  // sums of x^2 (q, k), of w g x (q, k)
-        const uint32_t tab_s = table_s + (uint32_t)(buf * a.r) * 4u;
-        if constexpr (NORM) {
+        const uint32_t sin_off = (uint32_t)a.r * 2u, run = (uint32_t)a.rot_units * H * 4u;  // bytes
+        const uint32_t tables = smem_u32(fix_p);
+        const float dq = (float)a.job[0].d, dk = (float)a.job[1].d;
+
+        int stage = 0, par = 0;
+        uint32_t phase = 0;
+        for (int64_t n = first_token; n < a.T; n += step) {
+            const bool ok = mbar_wait_fast(full + 8u * stage, phase, &g_rotary_error, a.wait_ns);
+            const uint32_t src = ring + (uint32_t)(stage * a.stage_bytes);
+            const uint32_t tab_s = tables + (uint32_t)(stage * tbytes);
+            float2 va[UPT][H], vb[UPT][H];  // x w (forward), x (gradients)
+            float2 ga[UPT][H], gb[UPT][H];  // gradients turned back
+            float2 sq[2] = {both(0.f), both(0.f)}, pg[2] = {both(0.f), both(0.f)};  // per job where mixed
 #pragma unroll
             for (int i = 0; i < UPT; ++i) {
-                float fa[E], fb[E];
-                Chunk<TA>::unpack(xa[i], fa);
-                Chunk<TA>::unpack(xb[i], fb);
-                float sq = 0.f, pg = 0.f;
+                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+                unpack2<TA, H>(off_a[i] >= 0 ? lds128(src + off_a[i]) : none, va[i]);
+                unpack2<TA, H>(off_b[i] >= 0 ? lds128(src + off_b[i]) : none, vb[i]);
+                if constexpr (NORM) {
+                    float2 q = both(0.f), r = both(0.f), w[H];
+                    weights(off_a[i] >= 0 ? off_a[i] : 0, w);
 #pragma unroll
-                for (int e = 0; e < E; ++e) sq = fmaf(fa[e], fa[e], sq);
+                    for (int p = 0; p < H; ++p) q = __ffma2_rn(va[i][p], va[i][p], q);
 #pragma unroll
-                for (int e = 0; e < E; ++e) sq = fmaf(fb[e], fb[e], sq);
-                if constexpr (BACK) {
-                    Chunk<TA>::unpack(off_a[i] >= 0 ? lds128(src + a.x_bytes + off_a[i]) : make_uint4(0u, 0u, 0u, 0u), ga[i]);
-                    Chunk<TA>::unpack(off_b[i] >= 0 ? lds128(src + a.x_bytes + off_b[i]) : make_uint4(0u, 0u, 0u, 0u), gb[i]);
-                    if (tab[i] >= 0) turn<E, HALF>(ga[i], gb[i], tab_s + tab[i], run, sin_off);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) pg = fmaf(fa[e] * ga[i][e], wa[i].get(e), pg);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) pg = fmaf(fb[e] * gb[i][e], wb[i].get(e), pg);
-                }
-                const bool k = (is_k >> i) & 1u;
-                acc.x += k ? 0.f : sq;
-                acc.y += k ? sq : 0.f;
-                acc.z += k ? 0.f : pg;
-                acc.w += k ? pg : 0.f;
-            }
-            for (int off = 16; off > 0; off >>= 1) {
-                acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
-                acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
-                if constexpr (BACK) {
-                    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, off);
-                    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, off);
-                }
-            }
-            if (a.warps > 1 && lane == 0) red[par * a.warps + gw] = acc;
-        }
-        const int next_buf = buf == 2 ? 0 : buf + 1;
-        if (a.r != 0 && n + step < a.T) {
-            fill(next_pos, next_buf);
-            next_pos = pos_at(n + 2 * step);
-        }
-        if (group_sync_or(!ok, group, a.warps)) break;
-        if (gt == 0 && n + (int64_t)a.stages * step < a.T) {
-            issue(n + (int64_t)a.stages * step, stage);
-            ++issued;
-        }
-        float inv_q = 1.f, inv_k = 1.f, cq = 0.f, ck = 0.f;
-        if constexpr (NORM) {
-            if (a.warps > 1) {
-                acc = red[par * a.warps];
-                for (int w = 1; w < a.warps; ++w) {
-                    const float4 v = red[par * a.warps + w];
-                    acc.x += v.x;
-                    acc.y += v.y;
+                    for (int p = 0; p < H; ++p) q = __ffma2_rn(vb[i][p], vb[i][p], q);
                     if constexpr (BACK) {
-                        acc.z += v.z;
-                        acc.w += v.w;
+                        unpack2<TA, H>(off_a[i] >= 0 ? lds128(src + a.x_bytes + off_a[i]) : none, ga[i]);
+                        unpack2<TA, H>(off_b[i] >= 0 ? lds128(src + a.x_bytes + off_b[i]) : none, gb[i]);
+                        if (tab[i] >= 0) turn<H, HALF, false>(ga[i], gb[i], tab_s + tab[i], run, sin_off, 1.f);
+#pragma unroll
+                        for (int p = 0; p < H; ++p) r = __ffma2_rn(__fmul2_rn(va[i][p], ga[i][p]), w[p], r);
+                        weights(off_b[i] >= 0 ? off_b[i] : 0, w);
+#pragma unroll
+                        for (int p = 0; p < H; ++p) r = __ffma2_rn(__fmul2_rn(vb[i][p], gb[i][p]), w[p], r);
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < H; ++p) va[i][p] = __fmul2_rn(va[i][p], w[p]);
+                        weights(off_b[i] >= 0 ? off_b[i] : 0, w);
+#pragma unroll
+                        for (int p = 0; p < H; ++p) vb[i][p] = __fmul2_rn(vb[i][p], w[p]);
+                    }
+                    if (mixed && ((is_k >> i) & 1u)) {
+                        sq[1] = __fadd2_rn(sq[1], q);
+                        if (BACK) pg[1] = __fadd2_rn(pg[1], r);
+                    } else {
+                        sq[0] = __fadd2_rn(sq[0], q);
+                        if (BACK) pg[0] = __fadd2_rn(pg[0], r);
                     }
                 }
             }
-            inv_q = rsqrtf(acc.x / (float)a.job[0].d + a.eps);
-            inv_k = a.njobs > 1 ? rsqrtf(acc.y / (float)a.job[1].d + a.eps) : 0.f;
-            if constexpr (BACK) {
-                cq = inv_q * inv_q * (acc.z / (float)a.job[0].d);
-                ck = a.njobs > 1 ? inv_k * inv_k * (acc.w / (float)a.job[1].d) : 0.f;
-            }
-        }
-        uint8_t *yq = a.job[0].y + n * a.job[0].ldy;
-        uint8_t *yk = a.job[1].y + n * a.job[1].ldy - a.job[1].row_off;
-#pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-            if (off_a[i] < 0) continue;
-            const bool k = (is_k >> i) & 1u;
-            uint8_t *y = k ? yk : yq;
-            float fa[E], fb[E];
-            Chunk<TA>::unpack_again(xa[i], fa);
-            Chunk<TA>::unpack_again(xb[i], fb);
-            if constexpr (BACK) {
-                const float inv = k ? inv_k : inv_q, c = k ? ck : cq;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    da[i][e] = fmaf(ga[i][e], fa[e] * inv, da[i][e]);
-                    db[i][e] = fmaf(gb[i][e], fb[e] * inv, db[i][e]);
-                    fa[e] = inv * (wa[i].get(e) * ga[i][e] - fa[e] * c);
-                    fb[e] = inv * (wb[i].get(e) * gb[i][e] - fb[e] * c);
+            float inv_q = 1.f, inv_k = 1.f, cq = 0.f, ck = 0.f;
+            bool failed = !ok;
+            if constexpr (NORM) {
+                float s0 = warp_sum(sq[0].x + sq[0].y), p0 = BACK ? warp_sum(pg[0].x + pg[0].y) : 0.f, s1 = 0.f, p1 = 0.f;
+                if (mixed) {
+                    s1 = warp_sum(sq[1].x + sq[1].y);
+                    if (BACK) p1 = warp_sum(pg[1].x + pg[1].y);
+                    failed = __any_sync(0xffffffffu, failed);
+                } else {
+                    // slots of this token: [x^2 | w g x][kSlots]; a job's warps only meet their own
+                    float *slot = red + par * 2 * kSlots;
+                    if (lane == 0) {
+                        slot[gw] = s0;
+                        if (BACK) slot[kSlots + gw] = p0;
+                    }
+                    failed = group_sync_or(failed, group, a.warps);
+                    s0 = s1 = p0 = p1 = 0.f;
+                    const int w0 = wk ? a.warps0 : 0, w1 = wk ? a.warps : a.warps0;
+                    for (int w = w0; w < w1; ++w) s0 += slot[w];
+                    if (BACK)
+                        for (int w = w0; w < w1; ++w) p0 += slot[kSlots + w];
+                    if (wk) {
+                        s1 = s0;
+                        p1 = p0;
+                    }
+                }
+                inv_q = rsqrtf(s0 / dq + a.eps);
+                inv_k = rsqrtf(s1 / dk + a.eps);
+                if constexpr (BACK) {
+                    cq = inv_q * inv_q * (p0 / dq);
+                    ck = inv_k * inv_k * (p1 / dk);
                 }
             } else {
-                if constexpr (NORM) {
-                    const float inv = k ? inv_k : inv_q;
+                failed = __any_sync(0xffffffffu, failed);
+            }
+            if (failed) break;
+            uint8_t *yq = a.job[0].y + n * a.job[0].ldy;
+            uint8_t *yk = a.job[1].y + n * a.job[1].ldy - a.job[1].row_off;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        fa[e] = (fa[e] * inv) * wa[i].get(e);
-                        fb[e] = (fb[e] * inv) * wb[i].get(e);
+            for (int i = 0; i < UPT; ++i) {
+                const bool k = mixed ? (is_k >> i) & 1u : wk;
+                const float inv = k ? inv_k : inv_q;
+                if constexpr (BACK) {
+                    const float2 nc = both(-(k ? ck : cq)), inv2 = both(inv);
+                    float2 w[H];
+                    weights(off_a[i] >= 0 ? off_a[i] : 0, w);
+#pragma unroll
+                    for (int p = 0; p < H; ++p) {
+                        da[i][p] = __ffma2_rn(ga[i][p], __fmul2_rn(va[i][p], inv2), da[i][p]);
+                        va[i][p] = __fmul2_rn(inv2, __ffma2_rn(va[i][p], nc, __fmul2_rn(w[p], ga[i][p])));
+                    }
+                    weights(off_b[i] >= 0 ? off_b[i] : 0, w);
+#pragma unroll
+                    for (int p = 0; p < H; ++p) {
+                        db[i][p] = __ffma2_rn(gb[i][p], __fmul2_rn(vb[i][p], inv2), db[i][p]);
+                        vb[i][p] = __fmul2_rn(inv2, __ffma2_rn(vb[i][p], nc, __fmul2_rn(w[p], gb[i][p])));
+                    }
+                } else if (tab[i] >= 0) {
+                    turn<H, HALF, NORM>(va[i], vb[i], tab_s + tab[i], run, sin_off, inv);
+                } else if (NORM) {
+#pragma unroll
+                    for (int p = 0; p < H; ++p) {
+                        va[i][p] = __fmul2_rn(va[i][p], both(inv));
+                        vb[i][p] = __fmul2_rn(vb[i][p], both(inv));
                     }
                 }
-                if (tab[i] >= 0) turn<E, HALF>(fa, fb, tab_s + tab[i], run, sin_off);
+                uint8_t *y = k ? yk : yq;
+                if (off_a[i] >= 0) st_stream_batched(y + off_a[i], pack2<TA, H>(va[i]));
+                if (off_b[i] >= 0) st_stream_batched(y + off_b[i], pack2<TA, H>(vb[i]));
             }
-            st_stream_batched(y + off_a[i], Chunk<TA>::pack(fa));
-            if (off_b[i] >= 0) st_stream_batched(y + off_b[i], Chunk<TA>::pack(fb));
+            __syncwarp();  // the warp has read the stage and its table
+            if (lane == 0) mbar_arrive(empty + 8u * stage);
+            if (++stage == a.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            par ^= 1;
         }
-        if (++stage == a.stages) {
-            stage = 0;
-            phase ^= 1u;
-        }
-        buf = next_buf;
-        par ^= 1;
     }
-    // after a wait that gave up: no copy may still be writing when the block exits
-    if (gt == 0 && n < a.T)
-        for (int64_t i = it; i < issued; ++i)
-            mbar_wait(bars + 8u * (uint32_t)(i % a.stages), (uint32_t)(i / a.stages) & 1u, &g_rotary_error, a.wait_ns);
 
     if constexpr (BACK) {
         // one row of partial sums per block: the groups' sums meet in the ring, added in group order
         const int dq = a.job[0].d, d = dq + (a.njobs > 1 ? a.job[1].d : 0);
         float *out = a.part + (int64_t)blockIdx.x * d;
-        float *mine = a.groups > 1 ? reinterpret_cast<float *>(smem) + (size_t)group * d : out;
+        float *mine = a.groups > 1 ? reinterpret_cast<float *>(rings) + (size_t)group * d : out;
         __syncthreads();  // every group has read its last stage
+        if (gw < a.warps) {
 #pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-            if (off_a[i] < 0) continue;
-            const bool k = (is_k >> i) & 1u;
-            const int col = k ? dq : 0, ro = k ? a.job[1].row_off : 0;
-            float *pa = mine + col + (off_a[i] - ro) / 16 * E;
+            for (int i = 0; i < UPT; ++i) {
+                if (off_a[i] < 0) continue;
+                const bool k = (is_k >> i) & 1u;
+                const int col = k ? dq : 0, ro = k ? a.job[1].row_off : 0;
+                float2 *pa = reinterpret_cast<float2 *>(mine + col + (off_a[i] - ro) / 16 * E);
 #pragma unroll
-            for (int e = 0; e < E; ++e) pa[e] = da[i][e];
-            if (off_b[i] >= 0) {
-                float *pb = mine + col + (off_b[i] - ro) / 16 * E;
+                for (int p = 0; p < H; ++p) pa[p] = da[i][p];
+                if (off_b[i] >= 0) {
+                    float2 *pb = reinterpret_cast<float2 *>(mine + col + (off_b[i] - ro) / 16 * E);
 #pragma unroll
-                for (int e = 0; e < E; ++e) pb[e] = db[i][e];
+                    for (int p = 0; p < H; ++p) pb[p] = db[i][p];
+                }
             }
         }
         if (a.groups > 1) {
             __syncthreads();
-            const float *all = reinterpret_cast<const float *>(smem);
+            const float *all = reinterpret_cast<const float *>(rings);
             for (int c = threadIdx.x; c < d; c += blockDim.x) {
                 float s = all[c];
                 for (int gi = 1; gi < a.groups; ++gi) s += all[(size_t)gi * d + c];
@@ -450,7 +532,8 @@ rotary_unit_kernel(const Params a) {
 
 struct Plan {
     bool fits;
-    int upt, warps, groups, ctas, stages, stage_bytes, x_bytes, smem;
+    int upt, warps, warps0, groups, threads;
+    bool wide;
 };
 
 constexpr int kMaxCtas = 4;  // blocks per SM at most (the partial gradients' rows are sized by it)
@@ -462,7 +545,6 @@ Plan plan(const Args &a, Params &p) {
     constexpr int E = Chunk<TA>::E;
     Plan r{};
     p.x_bytes = 0;
-    int units = 0;
     for (int i = 0; i < a.njobs; ++i) {
         const Job &j = a.job[i];
         Rows &J = p.job[i];
@@ -471,6 +553,7 @@ Plan plan(const Args &a, Params &p) {
             return r;
         if (MODE == kNormBack && (!aligned(j.g, 16) || j.ldg % 16)) return r;
         if (MODE != kRotate && !aligned(j.w, 4)) return r;
+        if ((int64_t)j.d * (int64_t)sizeof(TA) > kSmemLimit) return r;
         J.x = j.x;
         J.g = j.g;
         J.y = j.y;
@@ -479,7 +562,6 @@ Plan plan(const Args &a, Params &p) {
         J.ldg = j.ldg;
         J.ldy = j.ldy;
         J.d = j.d;
-        if ((int64_t)j.d * (int64_t)sizeof(TA) > kSmemLimit) return r;
         J.row_bytes = j.d * (int)sizeof(TA);
         J.row_off = p.x_bytes;
         p.x_bytes += J.row_bytes;
@@ -488,47 +570,73 @@ Plan plan(const Args &a, Params &p) {
         J.tail_units = (J.tail_chunks + 1) / 2;
         J.units_per_head = a.r / (2 * E) + J.tail_units;
         J.nunits = j.d / D * J.units_per_head;
-        units += J.nunits;
     }
     if (a.njobs == 1) p.job[1] = Rows{};
     p.stage_bytes = p.x_bytes * (MODE == kNormBack ? 2 : 1);
     p.rot_units = a.r / (2 * E);
-    r.upt = units <= 32 ? 1 : 2;
-    if (MODE != kNormBack && units > 32 * 2 * 16) r.upt = 4;
-    r.warps = (units + 32 * r.upt - 1) / (32 * r.upt);
-    if (r.warps > kMaxThreads / 32) return r;
-    r.groups = r.warps == 1 ? 8 : r.warps == 2 ? 4 : r.warps <= 4 ? 2 : 1;
-    const int threads = r.warps * r.groups * 32;
-    const int most = MODE == kNormBack || r.upt == 4 ? 512 : 768;
-    for (r.ctas = most / threads < 1 ? 1 : most / threads > kMaxCtas ? kMaxCtas : most / threads; r.ctas >= 1; --r.ctas) {
-        const int budget = kSmemLimit / r.ctas - 1024;  // the system keeps 1 KiB per block
-        for (r.stages = 8; r.stages >= 1; --r.stages) {
-            r.smem = r.groups * (r.stages * p.stage_bytes + group_fixed(a.r, r.warps, r.stages));
-            if (r.smem <= budget) break;
+    const int u0 = p.job[0].nunits, u1 = a.njobs > 1 ? p.job[1].nunits : 0;
+    auto warps_of = [](int units, int upt) { return (units + 32 * upt - 1) / (32 * upt); };
+    // two units of 16 bf16 elements or four of 8 fp32 a thread; half of that where one warp is
+    // enough for both tensors, twice that for rows too wide otherwise
+    constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
+    const int most = MODE == kNormBack ? kUsual : 4;
+    for (r.upt = u0 + u1 <= 16 * kUsual ? kUsual / 2 : kUsual; r.upt <= most; r.upt *= 2) {
+        if (u0 + u1 <= 32 * r.upt) {  // one warp for both tensors
+            r.warps0 = r.warps = 1;
+        } else {
+            r.warps0 = warps_of(u0, r.upt);
+            r.warps = r.warps0 + warps_of(u1, r.upt);
         }
-        if (r.stages >= 2 || (r.ctas == 1 && r.stages >= 1)) {
-            r.fits = true;
-            return r;
-        }
+        if (r.warps <= kMaxWarps) break;
     }
+    if (r.upt > most) return r;
+    r.wide = r.warps > 10;
+    r.groups = r.warps == 1 ? 4 : r.warps == 2 ? 3 : r.warps <= 4 ? 2 : 1;
+    r.threads = r.groups * (r.warps + 1) * 32;
+    r.fits = true;
     return r;
 }
 
-template <typename TA, typename TW, int MODE, int UPT, bool HALF>
-qkn_status launch_kernel(const Params &p, int grid, int threads, int smem, cudaStream_t s) {
-    static std::atomic<bool> attr_set[64];
+template <typename TA, typename TW, int MODE, int UPT, bool HALF, bool WIDE>
+qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bool *taken) {
+    const auto kernel = rotary_unit_kernel<TA, TW, MODE, UPT, HALF, WIDE>;
+    static std::atomic<int> registers[64];  // per device: registers per thread, 0 until asked
     int dev = 0;
     cudaGetDevice(&dev);
     const bool known = dev >= 0 && dev < 64;
-    if (!known || !attr_set[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(rotary_unit_kernel<TA, TW, MODE, UPT, HALF>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    int regs = known ? registers[dev].load(std::memory_order_acquire) : 0;
+    if (regs == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(rotary_unit_kernel)");
-        if (known) attr_set[dev].store(true, std::memory_order_release);
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes(rotary_unit_kernel)");
+        regs = fa.numRegs;
+        if (known) registers[dev].store(regs, std::memory_order_release);
     }
+    // as many blocks per SM as the registers hold (16384 per quarter of an SM, whole warps), with
+    // at least two stages each
+    int ctas = 16384 / ((regs + 7) / 8 * 8 * 32) * 4 / (r.threads / 32), smem = 0;
+    if (ctas > kMaxCtas) ctas = kMaxCtas;
+    if (ctas < 1) ctas = 1;
+    *taken = false;
+    for (; ctas >= 1 && !*taken; --ctas) {
+        const int budget = ctas == 1 ? kSmemLimit : 228 * 1024 / ctas - 1024;  // 1 KiB per block is the system's
+        for (p.stages = 8; p.stages >= 1; --p.stages) {
+            smem = p.w_bytes + r.groups * (p.stages * p.stage_bytes + group_fixed(p.r, p.stages));
+            if (smem <= budget) break;
+        }
+        if (p.stages >= 2 || (ctas == 1 && p.stages == 1)) {
+            *taken = true;
+            break;
+        }
+    }
+    if (!*taken) return QKN_OK;
+    const int64_t need = (p.T + r.groups - 1) / r.groups, cap = (int64_t)ctas * sm_count();
+    *grid = (int)(need < cap ? need : cap);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.gridDim = dim3((unsigned)*grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)r.threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr;
@@ -536,15 +644,15 @@ qkn_status launch_kernel(const Params &p, int grid, int threads, int smem, cudaS
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, rotary_unit_kernel<TA, TW, MODE, UPT, HALF>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
     if (e != cudaSuccess) return cuda_fail(e, "rotary_unit_kernel launch");
     return check_launch("rotary_unit_kernel launch");
 }
 
-template <typename TA, typename TW, int MODE, int UPT>
-qkn_status launch_layout(const Params &p, int layout, int grid, int threads, int smem, cudaStream_t s) {
-    return layout == QKN_ROTARY_HALF ? launch_kernel<TA, TW, MODE, UPT, true>(p, grid, threads, smem, s)
-                                     : launch_kernel<TA, TW, MODE, UPT, false>(p, grid, threads, smem, s);
+template <typename TA, typename TW, int MODE, int UPT, bool WIDE>
+qkn_status launch_layout(Params &p, const Plan &r, int layout, int *grid, cudaStream_t s, bool *taken) {
+    return layout == QKN_ROTARY_HALF ? launch_kernel<TA, TW, MODE, UPT, true, WIDE>(p, r, grid, s, taken)
+                                     : launch_kernel<TA, TW, MODE, UPT, false, WIDE>(p, r, grid, s, taken);
 }
 
 // Launches the unit kernel when it takes the call (*taken); *grid is its number of blocks.
@@ -565,15 +673,17 @@ qkn_status launch(const Args &a, bool *taken, int *grid, cudaStream_t s) {
     p.eps = a.eps;
     p.part = a.part;
     p.warps = r.warps;
+    p.warps0 = r.warps0;
     p.groups = r.groups;
-    p.stages = r.stages;
     p.wait_ns = kWaitTimeoutNs;
-    const int64_t need = (a.T + r.groups - 1) / r.groups, cap = (int64_t)r.ctas * sm_count();
-    *grid = (int)(need < cap ? need : cap);
-    const int threads = r.warps * r.groups * 32;
-    if (r.upt == 1) return launch_layout<TA, TW, MODE, 1>(p, a.layout, *grid, threads, r.smem, s);
-    if (r.upt == 2) return launch_layout<TA, TW, MODE, 2>(p, a.layout, *grid, threads, r.smem, s);
-    if constexpr (MODE != kNormBack) return launch_layout<TA, TW, MODE, 4>(p, a.layout, *grid, threads, r.smem, s);
+    p.w_bytes = MODE == kRotate ? 0 : ((p.job[0].d + p.job[1].d) * (int)sizeof(TW) + 15) / 16 * 16;
+    constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
+    if (r.upt < kUsual) return launch_layout<TA, TW, MODE, kUsual / 2, false>(p, r, a.layout, grid, s, taken);
+    if (r.upt == kUsual)
+        return r.wide ? launch_layout<TA, TW, MODE, kUsual, true>(p, r, a.layout, grid, s, taken)
+                      : launch_layout<TA, TW, MODE, kUsual, false>(p, r, a.layout, grid, s, taken);
+    if constexpr (MODE != kNormBack && kUsual < 4)
+        return launch_layout<TA, TW, MODE, 4, true>(p, r, a.layout, grid, s, taken);
     return fail(QKN_ERR_UNSUPPORTED, "rotary_unit_kernel: no variant for these rows");
 }
 
