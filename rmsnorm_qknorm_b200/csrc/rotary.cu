@@ -437,7 +437,7 @@ extern "C" QKN_API size_t qknorm_rotary_backward_workspace_bytes(int64_t T, int6
     // row factors of both tensors (element-wise kernels), then rows of partial sums: one per
     // slice of the element-wise kernel or per block of the unit kernel
     const size_t inv = ((size_t)T * 2 * 4 + 255) / 256 * 256;
-    const size_t blocks = (size_t)rot::unit::kMaxCtas * (size_t)sm_count();
+    const size_t blocks = (size_t)sm_count();
     const size_t parts = blocks > (size_t)rot::kScalarSlices ? blocks : (size_t)rot::kScalarSlices;
     return inv + ((size_t)T < parts ? (size_t)T : parts) * (size_t)(dq + dk) * 4;
 }

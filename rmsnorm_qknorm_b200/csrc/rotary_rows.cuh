@@ -68,7 +68,7 @@ struct Params {
     int warps, groups;       // consumer warps per group, groups per block
     int warps0;              // consumer warps of job 0 (== warps when one warp serves both jobs)
     int stages, stage_bytes, x_bytes;
-    int w_bytes;             // the block's copy of the weights, in front of the rings
+    int w_bytes, w_bf16;     // the block's fp32 copy of the weights, in front of the rings; their type in memory
     uint64_t wait_ns;
 };
 
@@ -76,9 +76,9 @@ constexpr int kMaxWarps = 15;  // consumer warps per group
 constexpr int kSlots = 16;     // sums per tensor and token
 
 inline __host__ __device__ int table_bytes(int r) { return (r * 4 + 15) / 16 * 16; }  // cos and sin of a token
-// per group: tables, 2 tokens x (sum x^2, sum w g x) x kSlots sums, full and empty barriers
+// per group: tables, 2 tokens x 2 tensors x (sum x^2, sum w g x) x kSlots sums, full and empty barriers
 inline __host__ __device__ int group_fixed(int r, int stages) {
-    return stages * table_bytes(r) + 4 * kSlots * 4 + stages * 16;
+    return stages * table_bytes(r) + 8 * kSlots * 4 + stages * 16;
 }
 
 __device__ __forceinline__ Rows pick(const Params &a, int which) {
@@ -154,59 +154,65 @@ __device__ __forceinline__ void lds_run(uint32_t addr, float2 (&f)[H / 2]) {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// cos and sin of a unit's two frequency runs.
+template <int H> struct Turns {
+    float2 c[H], s[H];
+    __device__ __forceinline__ void load(uint32_t cos_addr, uint32_t run, uint32_t sin_off) {
+        float2 t[H / 2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            lds_run<H>(cos_addr + (q ? run : 0u), t);
+#pragma unroll
+            for (int p = 0; p < H / 2; ++p) c[q * (H / 2) + p] = t[p];
+            lds_run<H>(cos_addr + sin_off + (q ? run : 0u), t);
+#pragma unroll
+            for (int p = 0; p < H / 2; ++p) s[q * (H / 2) + p] = t[p];
+        }
+    }
+};
+
 // The two chunks of a unit, turned and (SCALE) multiplied by inv.
 template <int H, bool HALF, bool SCALE>
-__device__ __forceinline__ void turn(float2 (&a)[H], float2 (&b)[H], uint32_t cos_addr, uint32_t run, uint32_t sin_off,
-                                     float inv) {
+__device__ __forceinline__ void turn(float2 (&a)[H], float2 (&b)[H], const Turns<H> &t, float inv) {
+    if constexpr (HALF) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        float2 c[H / 2], s[H / 2];
-        lds_run<H>(cos_addr + (q ? run : 0u), c);
-        lds_run<H>(cos_addr + sin_off + (q ? run : 0u), s);
-        if constexpr (HALF) {
-#pragma unroll
-            for (int p = 0; p < H / 2; ++p) {
-                const int i = q * (H / 2) + p;
-                const float2 x = a[i], y = b[i];
-                const float2 xc = __fmul2_rn(x, c[p]), ys = __fmul2_rn(y, s[p]), yc = __fmul2_rn(y, c[p]);
-                if constexpr (SCALE) {
-                    a[i] = __ffma2_rn(ys, both(-inv), __fmul2_rn(xc, both(inv)));
-                    b[i] = __fmul2_rn(__ffma2_rn(x, s[p], yc), both(inv));
-                } else {
-                    a[i] = __ffma2_rn(ys, both(-1.f), xc);
-                    b[i] = __ffma2_rn(x, s[p], yc);
-                }
+        for (int i = 0; i < H; ++i) {
+            const float2 x = a[i], y = b[i];
+            const float2 xc = __fmul2_rn(x, t.c[i]), ys = __fmul2_rn(y, t.s[i]), yc = __fmul2_rn(y, t.c[i]);
+            if constexpr (SCALE) {
+                a[i] = __ffma2_rn(ys, both(-inv), __fmul2_rn(xc, both(inv)));
+                b[i] = __fmul2_rn(__ffma2_rn(x, t.s[i], yc), both(inv));
+            } else {
+                a[i] = __ffma2_rn(ys, both(-1.f), xc);
+                b[i] = __ffma2_rn(x, t.s[i], yc);
             }
-        } else {
+        }
+    } else {
 #pragma unroll
-            for (int e = 0; e < H; ++e) {
-                const float ce = (e & 1) ? c[e >> 1].y : c[e >> 1].x, se = (e & 1) ? s[e >> 1].y : s[e >> 1].x;
-                const float2 v = q ? b[e] : a[e];
-                float2 t = make_float2(v.x * ce - v.y * se, v.y * ce + v.x * se);
-                if constexpr (SCALE) t = __fmul2_rn(t, both(inv));
-                if (q) b[e] = t;
-                else a[e] = t;
-            }
+        for (int i = 0; i < 2 * H; ++i) {  // chunk a's pairs take the first run, chunk b's the second
+            const int f = i;
+            const float ce = (f & 1) ? t.c[f >> 1].y : t.c[f >> 1].x, se = (f & 1) ? t.s[f >> 1].y : t.s[f >> 1].x;
+            const float2 v = i < H ? a[i % H] : b[i % H];
+            float2 r = make_float2(v.x * ce - v.y * se, v.y * ce + v.x * se);
+            if constexpr (SCALE) r = __fmul2_rn(r, both(inv));
+            if (i < H) a[i % H] = r;
+            else b[i % H] = r;
         }
     }
 }
 
-// The weights of a chunk from shared memory, as pairs.
-template <typename TW, int H>
-__device__ __forceinline__ void lds_weights(uint32_t addr, float2 (&f)[H]) {
-    if constexpr (sizeof(TW) * 2 * H == 32) {  // fp32 weights of 8 elements
-        const uint4 a = lds128(addr), b = lds128(addr + 16);
-        f[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
-        f[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+// The weights of a chunk from shared memory, as pairs.  They are kept as fp32,
+// the first four of every chunk in one array and, for chunks of eight, the
+// others `upper` bytes behind: neighbouring threads read neighbouring words.
+template <int H>
+__device__ __forceinline__ void lds_weights(uint32_t addr, uint32_t upper, float2 (&f)[H]) {
+    const uint4 a = lds128(addr);
+    f[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+    f[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+    if constexpr (H == 4) {
+        const uint4 b = lds128(addr + upper);
         f[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
         f[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
-    } else if constexpr (sizeof(TW) * 2 * H == 16) {
-        unpack2<TW, H>(lds128(addr), f);
-    } else {  // bf16 weights of 4 elements
-        uint2 v;
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-        f[0] = make_float2(bf16lo(v.x), bf16hi(v.x));
-        f[1] = make_float2(bf16lo(v.y), bf16hi(v.y));
     }
 }
 
@@ -215,18 +221,13 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// WIDE: groups of up to 15 consumer warps; otherwise up to 10, two blocks per SM where the registers allow.
-template <bool WIDE> constexpr int max_threads() { return WIDE ? 32 * (kMaxWarps + 1) : 32 * 11; }
-#ifndef ROT_MINB
-#define ROT_MINB 2
-#endif
-#ifndef ROT_MINB_BACK
-#define ROT_MINB_BACK 1
-#endif
+// Threads of a block: 20 warps leave a thread 96 registers, 16 warps 128 (the
+// gradients, and the variant with twice the units).
+template <int MODE, int UPT, int E> constexpr int max_threads() { return MODE == kNormBack || UPT * E > 16 ? 512 : 640; }
 
-template <typename TA, typename TW, int MODE, int UPT, bool HALF, bool WIDE>
-__global__ void __launch_bounds__(max_threads<WIDE>(), WIDE ? 1 : MODE == kNormBack ? ROT_MINB_BACK : ROT_MINB)
-rotary_unit_kernel(const Params a) {
+// MIXED: one warp serves both tensors; otherwise q and k have warps of their own.
+template <typename TA, int MODE, int UPT, bool HALF, bool MIXED>
+__global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rotary_unit_kernel(const Params a) {
     constexpr int E = Chunk<TA>::E, H = E / 2;
     constexpr bool NORM = MODE != kRotate, BACK = MODE == kNormBack;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -238,26 +239,54 @@ rotary_unit_kernel(const Params a) {
     const uint32_t ring = smem_u32(rings + (size_t)group * a.stages * a.stage_bytes);
     const int tbytes = table_bytes(a.r);
     float *red = reinterpret_cast<float *>(fix_p + (size_t)a.stages * tbytes);
-    const uint32_t full = smem_u32(red + 4 * kSlots), empty = full + 8u * a.stages;
+    const uint32_t full = smem_u32(red + 8 * kSlots), empty = full + 8u * a.stages;
     const int64_t step = (int64_t)gridDim.x * a.groups;
-    const int64_t first_token = (int64_t)blockIdx.x * a.groups + group;
+    const int64_t first_token = (int64_t)group * gridDim.x + blockIdx.x;  // few tokens spread over the SMs first
 
-    if (gt == 0) {
+    // copies of a token's rows into a stage (one lane)
+    auto fill = [&](int64_t n, int stage) {
+        const uint32_t bar = full + 8u * stage, dst = ring + (uint32_t)(stage * a.stage_bytes);
+        mbar_arrive_expect_tx(bar, (uint32_t)a.stage_bytes);
+        bulk_g2s(dst, a.job[0].x + n * a.job[0].ldx, a.job[0].row_bytes, bar);
+        if (BACK) bulk_g2s(dst + a.x_bytes, a.job[0].g + n * a.job[0].ldg, a.job[0].row_bytes, bar);
+        if (a.njobs > 1) {
+            bulk_g2s(dst + a.job[1].row_off, a.job[1].x + n * a.job[1].ldx, a.job[1].row_bytes, bar);
+            if (BACK)
+                bulk_g2s(dst + a.x_bytes + a.job[1].row_off, a.job[1].g + n * a.job[1].ldg, a.job[1].row_bytes, bar);
+        }
+    };
+    uint32_t issued = 0;  // stages filled (the producer's lane 0)
+    if (gw == a.warps && lane == 0) {
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(full + 8u * s, 2);         // the producer's two arrivals and the copies' bytes
             mbar_init(empty + 8u * s, a.warps);  // one per consumer warp
         }
         mbar_init_fence();
+        // the previous kernel on the stream has finished before any global memory is touched
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        int64_t n = first_token;
+        for (int s = 0; s < a.stages && n < a.T; ++s, n += step) {
+            fill(n, s);
+            issued |= 1u << s;
+        }
     }
-    for (int i = gt; i < 4 * kSlots; i += gthreads) red[i] = 0.f;
-    // the previous kernel on the stream has finished before any global memory is touched
+    for (int i = gt; i < 8 * kSlots; i += gthreads) red[i] = 0.f;
+    const int chunks0 = a.job[0].row_bytes / 16, chunks = a.x_bytes / 16;
+    if (threadIdx.x < 4) reinterpret_cast<float *>(smem)[NORM ? chunks * E + threadIdx.x : threadIdx.x] = 0.f;  // zeros
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if constexpr (NORM) {  // weights word by word, at the element positions of a stage's rows
-        const int d0 = a.job[0].d, words = (int)sizeof(TW) * (d0 + a.job[1].d) / 4, words0 = (int)sizeof(TW) * d0 / 4;
-        for (int i = threadIdx.x; i < words; i += blockDim.x)
-            reinterpret_cast<uint32_t *>(smem)[i] = i < words0 ? __ldg(static_cast<const uint32_t *>(a.job[0].w) + i)
-                                                               : __ldg(static_cast<const uint32_t *>(a.job[1].w) + i - words0);
+    if constexpr (NORM) {
+        float4 *w = reinterpret_cast<float4 *>(smem);
+        for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+            const bool k = c >= chunks0;
+            const void *src = k ? a.job[1].w : a.job[0].w;
+            const int at = (c - (k ? chunks0 : 0)) * E;
+            float f[E];
+            if (a.w_bf16) load_weights_batched<__nv_bfloat16, E>(static_cast<const __nv_bfloat16 *>(src) + at, f);
+            else load_weights_batched<float, E>(static_cast<const float *>(src) + at, f);
+#pragma unroll
+            for (int q = 0; q < E / 4; ++q) w[q * chunks + c] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+        }
     }
     __syncthreads();
 
@@ -286,24 +315,15 @@ rotary_unit_kernel(const Params a) {
                            : (int64_t)__ldg(static_cast<const int *>(a.pos) + n);
         };
         int stage = 0;
-        uint32_t phase = 0, issued = 0;
+        uint32_t phase = 0;
+        bool first = true;  // the first round of stages is filled already
         int64_t p = pos_at(first_token);
         for (int64_t n = first_token; n < a.T; n += step) {
-            bool ok = mbar_wait_fast(empty + 8u * stage, phase ^ 1u, &g_rotary_error, a.wait_ns);
-            if (__any_sync(0xffffffffu, !ok)) break;
             const uint32_t bar = full + 8u * stage;
-            if (lane == 0) {
-                const uint32_t dst = ring + (uint32_t)(stage * a.stage_bytes);
-                mbar_arrive_expect_tx(bar, (uint32_t)a.stage_bytes);
-                bulk_g2s(dst, a.job[0].x + n * a.job[0].ldx, a.job[0].row_bytes, bar);
-                if (BACK) bulk_g2s(dst + a.x_bytes, a.job[0].g + n * a.job[0].ldg, a.job[0].row_bytes, bar);
-                if (a.njobs > 1) {
-                    bulk_g2s(dst + a.job[1].row_off, a.job[1].x + n * a.job[1].ldx, a.job[1].row_bytes, bar);
-                    if (BACK)
-                        bulk_g2s(dst + a.x_bytes + a.job[1].row_off, a.job[1].g + n * a.job[1].ldg, a.job[1].row_bytes,
-                                 bar);
-                }
-                issued |= 1u << stage;
+            if (!first) {
+                const bool ok = mbar_wait_fast(empty + 8u * stage, phase ^ 1u, &g_rotary_error, a.wait_ns);
+                if (__any_sync(0xffffffffu, !ok)) break;
+                if (lane == 0) fill(n, stage);
             }
             const int64_t next = pos_at(n + step);
             float *t = reinterpret_cast<float *>(fix_p + (size_t)stage * tbytes);
@@ -318,23 +338,26 @@ rotary_unit_kernel(const Params a) {
             if (++stage == a.stages) {
                 stage = 0;
                 phase ^= 1u;
+                first = false;
             }
         }
         // no copy may still be writing when the block exits: the last phase filled on every stage
-        // (on the normal path the consumers have waited for them all already)
+        // (on the normal path the consumers have waited for them all already).  Stages behind
+        // `stage` were last filled in the round before, or, in the first round, in this one
         if (lane == 0)
             for (int s = 0; s < a.stages; ++s)
-                if (issued & (1u << s)) mbar_wait(full + 8u * s, s < stage ? phase : phase ^ 1u, &g_rotary_error, a.wait_ns);
+                if (issued & (1u << s))
+                    mbar_wait(full + 8u * s, s < stage || first ? phase : phase ^ 1u, &g_rotary_error, a.wait_ns);
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- consumer warps
-        const bool mixed = a.warps0 == a.warps && a.njobs > 1;  // one warp serves both jobs
+        const bool wk = !MIXED && gw >= a.warps0;  // a warp of the keys
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-            int which = mixed ? 0 : (gw >= a.warps0 ? 1 : 0);
-            const int jw = which ? a.warps - a.warps0 : a.warps0;
-            int u = gt - (which ? a.warps0 * 32 : 0) + i * jw * 32;
-            if (mixed && u >= a.job[0].nunits) {
+            int which = wk ? 1 : 0;
+            const int jw = wk ? a.warps - a.warps0 : a.warps0;
+            int u = gt - (wk ? a.warps0 * 32 : 0) + i * jw * 32;
+            if (MIXED && u >= a.job[0].nunits) {
                 u -= a.job[0].nunits;
                 which = 1;
             }
@@ -354,10 +377,6 @@ rotary_unit_kernel(const Params a) {
                 if (t + J.tail_units < J.tail_chunks) off_b[i] = off_a[i] + J.tail_units * 16;
             }
         }
-        const bool wk = !mixed && gw >= a.warps0;  // a warp of job 1 alone
-        const uint32_t w_s = smem_u32(smem);
-        // a chunk's weights: 16 bytes of elements are E weights
-        auto weights = [&](int off, float2 (&f)[H]) { lds_weights<TW, H>(w_s + (uint32_t)(off / 16 * (E * (int)sizeof(TW))), f); };
         if constexpr (BACK) {
 #pragma unroll
             for (int i = 0; i < UPT; ++i)
@@ -365,8 +384,21 @@ rotary_unit_kernel(const Params a) {
                 for (int p = 0; p < H; ++p) da[i][p] = db[i][p] = make_float2(0.f, 0.f);
         }
         const uint32_t sin_off = (uint32_t)a.r * 2u, run = (uint32_t)a.rot_units * H * 4u;  // bytes
-        const uint32_t tables = smem_u32(fix_p);
-        const float dq = (float)a.job[0].d, dk = (float)a.job[1].d;
+        const uint32_t tables = smem_u32(fix_p), w_s = smem_u32(smem), upper = (uint32_t)chunks * 16u;
+        // a chunk that is not there reads zeros (behind the weights) and stores nothing
+        const uint32_t zeros = w_s + (NORM ? (uint32_t)(chunks * E * 4) : 0u);
+        // a thread's units lie at the same place of their heads when a head's units divide the
+        // warps' stride (powers of two do): cos and sin are then read once per token
+        bool same = true;
+#pragma unroll
+        for (int i = 1; i < UPT; ++i) same = same && (off_a[i] < 0 || tab[i] == tab[0]);
+        same = __all_sync(0xffffffffu, same);
+        const float d_q = (float)a.job[0].d, d_k = (float)a.job[1].d;
+        // rows of the results, moved by the chunk's place in a stage
+        uint8_t *yq = (wk ? a.job[1].y - a.job[1].row_off : a.job[0].y) + first_token * (wk ? a.job[1].ldy : a.job[0].ldy);
+        uint8_t *yk = MIXED ? a.job[1].y - a.job[1].row_off + first_token * a.job[1].ldy : nullptr;
+        const int64_t yq_step = step * (wk ? a.job[1].ldy : a.job[0].ldy), yk_step = step * a.job[1].ldy;
+        const int my_warps = wk ? a.warps - a.warps0 : a.warps0, my_warp = wk ? gw - a.warps0 : gw;
 
         int stage = 0, par = 0;
         uint32_t phase = 0;
@@ -374,116 +406,140 @@ rotary_unit_kernel(const Params a) {
             const bool ok = mbar_wait_fast(full + 8u * stage, phase, &g_rotary_error, a.wait_ns);
             const uint32_t src = ring + (uint32_t)(stage * a.stage_bytes);
             const uint32_t tab_s = tables + (uint32_t)(stage * tbytes);
-            float2 va[UPT][H], vb[UPT][H];  // x w (forward), x (gradients)
-            float2 ga[UPT][H], gb[UPT][H];  // gradients turned back
-            float2 sq[2] = {both(0.f), both(0.f)}, pg[2] = {both(0.f), both(0.f)};  // per job where mixed
+            float2 va[UPT][H], vb[UPT][H];  // rotary: x; with the norm: x w; gradients: dy turned back
+            float2 sq[2] = {both(0.f), both(0.f)}, pg[2] = {both(0.f), both(0.f)};  // sums of x^2 and of w g x
+            Turns<H> cs;
+            if (BACK && same && tab[0] >= 0) cs.load(tab_s + tab[0], run, sin_off);
 #pragma unroll
             for (int i = 0; i < UPT; ++i) {
-                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-                unpack2<TA, H>(off_a[i] >= 0 ? lds128(src + off_a[i]) : none, va[i]);
-                unpack2<TA, H>(off_b[i] >= 0 ? lds128(src + off_b[i]) : none, vb[i]);
-                if constexpr (NORM) {
-                    float2 q = both(0.f), r = both(0.f), w[H];
-                    weights(off_a[i] >= 0 ? off_a[i] : 0, w);
+                const uint32_t pa = off_a[i] >= 0 ? src + off_a[i] : zeros, pb = off_b[i] >= 0 ? src + off_b[i] : zeros;
+                const uint32_t qa = w_s + max(off_a[i], 0), qb = w_s + max(off_b[i], 0);
+                const int m = MIXED ? (is_k >> i) & 1u : 0;
+                if constexpr (MODE == kRotate) {
+                    unpack2<TA, H>(lds128(pa), va[i]);
+                    unpack2<TA, H>(lds128(pb), vb[i]);
+                } else if constexpr (MODE == kNorm) {
+                    float2 q = both(0.f), w[H];
+                    unpack2<TA, H>(lds128(pa), va[i]);
+                    lds_weights<H>(qa, upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) q = __ffma2_rn(va[i][p], va[i][p], q);
 #pragma unroll
+                    for (int p = 0; p < H; ++p) va[i][p] = __fmul2_rn(va[i][p], w[p]);
+                    unpack2<TA, H>(lds128(pb), vb[i]);
+                    lds_weights<H>(qb, upper, w);
+#pragma unroll
                     for (int p = 0; p < H; ++p) q = __ffma2_rn(vb[i][p], vb[i][p], q);
-                    if constexpr (BACK) {
-                        unpack2<TA, H>(off_a[i] >= 0 ? lds128(src + a.x_bytes + off_a[i]) : none, ga[i]);
-                        unpack2<TA, H>(off_b[i] >= 0 ? lds128(src + a.x_bytes + off_b[i]) : none, gb[i]);
-                        if (tab[i] >= 0) turn<H, HALF, false>(ga[i], gb[i], tab_s + tab[i], run, sin_off, 1.f);
 #pragma unroll
-                        for (int p = 0; p < H; ++p) r = __ffma2_rn(__fmul2_rn(va[i][p], ga[i][p]), w[p], r);
-                        weights(off_b[i] >= 0 ? off_b[i] : 0, w);
-#pragma unroll
-                        for (int p = 0; p < H; ++p) r = __ffma2_rn(__fmul2_rn(vb[i][p], gb[i][p]), w[p], r);
-                    } else {
-#pragma unroll
-                        for (int p = 0; p < H; ++p) va[i][p] = __fmul2_rn(va[i][p], w[p]);
-                        weights(off_b[i] >= 0 ? off_b[i] : 0, w);
-#pragma unroll
-                        for (int p = 0; p < H; ++p) vb[i][p] = __fmul2_rn(vb[i][p], w[p]);
+                    for (int p = 0; p < H; ++p) vb[i][p] = __fmul2_rn(vb[i][p], w[p]);
+                    if (m) sq[1] = __fadd2_rn(sq[1], q);
+                    else sq[0] = __fadd2_rn(sq[0], q);
+                } else {
+                    unpack2<TA, H>(lds128(off_a[i] >= 0 ? pa + a.x_bytes : zeros), va[i]);
+                    unpack2<TA, H>(lds128(off_b[i] >= 0 ? pb + a.x_bytes : zeros), vb[i]);
+                    if (tab[i] >= 0) {
+                        if (!same) cs.load(tab_s + tab[i], run, sin_off);
+                        turn<H, HALF, false>(va[i], vb[i], cs, 1.f);
                     }
-                    if (mixed && ((is_k >> i) & 1u)) {
+                    float2 q = both(0.f), r = both(0.f), w[H], x[H];
+                    unpack2<TA, H>(lds128(pa), x);
+                    lds_weights<H>(qa, upper, w);
+#pragma unroll
+                    for (int p = 0; p < H; ++p) {
+                        q = __ffma2_rn(x[p], x[p], q);
+                        r = __ffma2_rn(__fmul2_rn(x[p], va[i][p]), w[p], r);
+                    }
+                    unpack2<TA, H>(lds128(pb), x);
+                    lds_weights<H>(qb, upper, w);
+#pragma unroll
+                    for (int p = 0; p < H; ++p) {
+                        q = __ffma2_rn(x[p], x[p], q);
+                        r = __ffma2_rn(__fmul2_rn(x[p], vb[i][p]), w[p], r);
+                    }
+                    if (m) {
                         sq[1] = __fadd2_rn(sq[1], q);
-                        if (BACK) pg[1] = __fadd2_rn(pg[1], r);
+                        pg[1] = __fadd2_rn(pg[1], r);
                     } else {
                         sq[0] = __fadd2_rn(sq[0], q);
-                        if (BACK) pg[0] = __fadd2_rn(pg[0], r);
+                        pg[0] = __fadd2_rn(pg[0], r);
                     }
                 }
             }
             float inv_q = 1.f, inv_k = 1.f, cq = 0.f, ck = 0.f;
             bool failed = !ok;
             if constexpr (NORM) {
-                float s0 = warp_sum(sq[0].x + sq[0].y), p0 = BACK ? warp_sum(pg[0].x + pg[0].y) : 0.f, s1 = 0.f, p1 = 0.f;
-                if (mixed) {
-                    s1 = warp_sum(sq[1].x + sq[1].y);
-                    if (BACK) p1 = warp_sum(pg[1].x + pg[1].y);
+                float s = warp_sum(sq[0].x + sq[0].y), t = BACK ? warp_sum(pg[0].x + pg[0].y) : 0.f;
+                if constexpr (MIXED) {
+                    inv_k = rsqrtf(warp_sum(sq[1].x + sq[1].y) / d_k + a.eps);
+                    if (BACK) ck = inv_k * inv_k * (warp_sum(pg[1].x + pg[1].y) / d_k);
                     failed = __any_sync(0xffffffffu, failed);
                 } else {
-                    // slots of this token: [x^2 | w g x][kSlots]; a job's warps only meet their own
-                    float *slot = red + par * 2 * kSlots;
+                    // the sums of this token: [q | k][x^2 | w g x][kSlots], slots without a warp hold zero
+                    float *slot = red + (par * 4 + (wk ? 2 : 0)) * kSlots;
                     if (lane == 0) {
-                        slot[gw] = s0;
-                        if (BACK) slot[kSlots + gw] = p0;
+                        slot[my_warp] = s;
+                        if (BACK) slot[kSlots + my_warp] = t;
                     }
                     failed = group_sync_or(failed, group, a.warps);
-                    s0 = s1 = p0 = p1 = 0.f;
-                    const int w0 = wk ? a.warps0 : 0, w1 = wk ? a.warps : a.warps0;
-                    for (int w = w0; w < w1; ++w) s0 += slot[w];
-                    if (BACK)
-                        for (int w = w0; w < w1; ++w) p0 += slot[kSlots + w];
-                    if (wk) {
-                        s1 = s0;
-                        p1 = p0;
+                    s = t = 0.f;
+                    for (int w = 0; w < my_warps; w += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(slot + w);
+                        s = (((s + v.x) + v.y) + v.z) + v.w;
+                        if constexpr (BACK) {
+                            const float4 u = *reinterpret_cast<const float4 *>(slot + kSlots + w);
+                            t = (((t + u.x) + u.y) + u.z) + u.w;
+                        }
                     }
                 }
-                inv_q = rsqrtf(s0 / dq + a.eps);
-                inv_k = rsqrtf(s1 / dk + a.eps);
-                if constexpr (BACK) {
-                    cq = inv_q * inv_q * (p0 / dq);
-                    ck = inv_k * inv_k * (p1 / dk);
-                }
+                const float d = wk ? d_k : d_q;
+                inv_q = rsqrtf(s / d + a.eps);
+                if (BACK) cq = inv_q * inv_q * (t / d);
             } else {
                 failed = __any_sync(0xffffffffu, failed);
             }
             if (failed) break;
-            uint8_t *yq = a.job[0].y + n * a.job[0].ldy;
-            uint8_t *yk = a.job[1].y + n * a.job[1].ldy - a.job[1].row_off;
+            if (!BACK && same && tab[0] >= 0) cs.load(tab_s + tab[0], run, sin_off);
 #pragma unroll
             for (int i = 0; i < UPT; ++i) {
-                const bool k = mixed ? (is_k >> i) & 1u : wk;
-                const float inv = k ? inv_k : inv_q;
+                const bool m = MIXED && ((is_k >> i) & 1u);
+                const float inv = m ? inv_k : inv_q;
+                uint8_t *y = m ? yk : yq;
                 if constexpr (BACK) {
-                    const float2 nc = both(-(k ? ck : cq)), inv2 = both(inv);
-                    float2 w[H];
-                    weights(off_a[i] >= 0 ? off_a[i] : 0, w);
+                    const float2 nc = both(-(m ? ck : cq)), inv2 = both(inv);
+                    float2 w[H], x[H];
+                    unpack2<TA, H>(lds128(off_a[i] >= 0 ? src + off_a[i] : zeros), x);
+                    lds_weights<H>(w_s + max(off_a[i], 0), upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) {
-                        da[i][p] = __ffma2_rn(ga[i][p], __fmul2_rn(va[i][p], inv2), da[i][p]);
-                        va[i][p] = __fmul2_rn(inv2, __ffma2_rn(va[i][p], nc, __fmul2_rn(w[p], ga[i][p])));
+                        da[i][p] = __ffma2_rn(va[i][p], __fmul2_rn(x[p], inv2), da[i][p]);
+                        va[i][p] = __fmul2_rn(inv2, __ffma2_rn(x[p], nc, __fmul2_rn(w[p], va[i][p])));
                     }
-                    weights(off_b[i] >= 0 ? off_b[i] : 0, w);
+                    if (off_a[i] >= 0) st_stream_batched(y + off_a[i], pack2<TA, H>(va[i]));
+                    unpack2<TA, H>(lds128(off_b[i] >= 0 ? src + off_b[i] : zeros), x);
+                    lds_weights<H>(w_s + max(off_b[i], 0), upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) {
-                        db[i][p] = __ffma2_rn(gb[i][p], __fmul2_rn(vb[i][p], inv2), db[i][p]);
-                        vb[i][p] = __fmul2_rn(inv2, __ffma2_rn(vb[i][p], nc, __fmul2_rn(w[p], gb[i][p])));
+                        db[i][p] = __ffma2_rn(vb[i][p], __fmul2_rn(x[p], inv2), db[i][p]);
+                        vb[i][p] = __fmul2_rn(inv2, __ffma2_rn(x[p], nc, __fmul2_rn(w[p], vb[i][p])));
                     }
-                } else if (tab[i] >= 0) {
-                    turn<H, HALF, NORM>(va[i], vb[i], tab_s + tab[i], run, sin_off, inv);
-                } else if (NORM) {
+                    if (off_b[i] >= 0) st_stream_batched(y + off_b[i], pack2<TA, H>(vb[i]));
+                } else {
+                    if (tab[i] >= 0) {
+                        if (!same) cs.load(tab_s + tab[i], run, sin_off);
+                        turn<H, HALF, NORM>(va[i], vb[i], cs, inv);
+                    } else if (NORM) {
 #pragma unroll
-                    for (int p = 0; p < H; ++p) {
-                        va[i][p] = __fmul2_rn(va[i][p], both(inv));
-                        vb[i][p] = __fmul2_rn(vb[i][p], both(inv));
+                        for (int p = 0; p < H; ++p) {
+                            va[i][p] = __fmul2_rn(va[i][p], both(inv));
+                            vb[i][p] = __fmul2_rn(vb[i][p], both(inv));
+                        }
                     }
+                    if (off_a[i] >= 0) st_stream_batched(y + off_a[i], pack2<TA, H>(va[i]));
+                    if (off_b[i] >= 0) st_stream_batched(y + off_b[i], pack2<TA, H>(vb[i]));
                 }
-                uint8_t *y = k ? yk : yq;
-                if (off_a[i] >= 0) st_stream_batched(y + off_a[i], pack2<TA, H>(va[i]));
-                if (off_b[i] >= 0) st_stream_batched(y + off_b[i], pack2<TA, H>(vb[i]));
             }
+            yq += yq_step;
+            if (MIXED) yk += yk_step;
             __syncwarp();  // the warp has read the stage and its table
             if (lane == 0) mbar_arrive(empty + 8u * stage);
             if (++stage == a.stages) {
@@ -533,15 +589,13 @@ rotary_unit_kernel(const Params a) {
 struct Plan {
     bool fits;
     int upt, warps, warps0, groups, threads;
-    bool wide;
+    bool mixed;
 };
-
-constexpr int kMaxCtas = 4;  // blocks per SM at most (the partial gradients' rows are sized by it)
 
 // Whether the unit kernel takes the call, and its geometry: a rule on the
 // rows' widths, types and alignment, never on the number of tokens.
-template <typename TA, typename TW, int MODE>
-Plan plan(const Args &a, Params &p) {
+template <typename TA, int MODE>
+Plan plan(const Args &a, Params &p, size_t w_size) {
     constexpr int E = Chunk<TA>::E;
     Plan r{};
     p.x_bytes = 0;
@@ -552,8 +606,8 @@ Plan plan(const Args &a, Params &p) {
         if (D % E != 0 || a.r % (2 * E) != 0 || !aligned(j.x, 16) || !aligned(j.y, 16) || j.ldx % 16 || j.ldy % 16)
             return r;
         if (MODE == kNormBack && (!aligned(j.g, 16) || j.ldg % 16)) return r;
-        if (MODE != kRotate && !aligned(j.w, 4)) return r;
-        if ((int64_t)j.d * (int64_t)sizeof(TA) > kSmemLimit) return r;
+        if (MODE != kRotate && !aligned(j.w, E * w_size < 16 ? E * w_size : 16)) return r;
+                if ((int64_t)j.d * (int64_t)sizeof(TA) > kSmemLimit) return r;
         J.x = j.x;
         J.g = j.g;
         J.y = j.y;
@@ -576,64 +630,49 @@ Plan plan(const Args &a, Params &p) {
     p.rot_units = a.r / (2 * E);
     const int u0 = p.job[0].nunits, u1 = a.njobs > 1 ? p.job[1].nunits : 0;
     auto warps_of = [](int units, int upt) { return (units + 32 * upt - 1) / (32 * upt); };
-    // two units of 16 bf16 elements or four of 8 fp32 a thread; half of that where one warp is
-    // enough for both tensors, twice that for rows too wide otherwise
+    // two units of 16 bf16 elements or four of 8 fp32 a thread, twice that for rows too wide
+    // otherwise; rows of both tensors that one warp holds share it
     constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
     const int most = MODE == kNormBack ? kUsual : 4;
-    for (r.upt = u0 + u1 <= 16 * kUsual ? kUsual / 2 : kUsual; r.upt <= most; r.upt *= 2) {
-        if (u0 + u1 <= 32 * r.upt) {  // one warp for both tensors
-            r.warps0 = r.warps = 1;
-        } else {
+    r.upt = kUsual;
+    if (a.njobs > 1 && u0 + u1 <= 32 * kUsual) {
+        r.mixed = true;
+        r.warps0 = r.warps = 1;
+    } else {
+        for (;; r.upt *= 2) {
+            if (r.upt > most) return r;
             r.warps0 = warps_of(u0, r.upt);
             r.warps = r.warps0 + warps_of(u1, r.upt);
+            if (r.warps <= kMaxWarps) break;
         }
-        if (r.warps <= kMaxWarps) break;
     }
-    if (r.upt > most) return r;
-    r.wide = r.warps > 10;
-    r.groups = r.warps == 1 ? 4 : r.warps == 2 ? 3 : r.warps <= 4 ? 2 : 1;
+    // groups side by side in a block (one block per SM, so that they share the weights' copy)
+    r.groups = (MODE == kNormBack || r.upt * E > 16 ? 16 : 20) / (r.warps + 1);
     r.threads = r.groups * (r.warps + 1) * 32;
     r.fits = true;
     return r;
 }
 
-template <typename TA, typename TW, int MODE, int UPT, bool HALF, bool WIDE>
+template <typename TA, int MODE, int UPT, bool HALF, bool MIXED>
 qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bool *taken) {
-    const auto kernel = rotary_unit_kernel<TA, TW, MODE, UPT, HALF, WIDE>;
-    static std::atomic<int> registers[64];  // per device: registers per thread, 0 until asked
+    const auto kernel = rotary_unit_kernel<TA, MODE, UPT, HALF, MIXED>;
+    static std::atomic<bool> attr_set[64];
     int dev = 0;
     cudaGetDevice(&dev);
     const bool known = dev >= 0 && dev < 64;
-    int regs = known ? registers[dev].load(std::memory_order_acquire) : 0;
-    if (regs == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (!known || !attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(rotary_unit_kernel)");
-        cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, kernel);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes(rotary_unit_kernel)");
-        regs = fa.numRegs;
-        if (known) registers[dev].store(regs, std::memory_order_release);
+        if (known) attr_set[dev].store(true, std::memory_order_release);
     }
-    // as many blocks per SM as the registers hold (16384 per quarter of an SM, whole warps), with
-    // at least two stages each
-    int ctas = 16384 / ((regs + 7) / 8 * 8 * 32) * 4 / (r.threads / 32), smem = 0;
-    if (ctas > kMaxCtas) ctas = kMaxCtas;
-    if (ctas < 1) ctas = 1;
-    *taken = false;
-    for (; ctas >= 1 && !*taken; --ctas) {
-        const int budget = ctas == 1 ? kSmemLimit : 228 * 1024 / ctas - 1024;  // 1 KiB per block is the system's
-        for (p.stages = 8; p.stages >= 1; --p.stages) {
-            smem = p.w_bytes + r.groups * (p.stages * p.stage_bytes + group_fixed(p.r, p.stages));
-            if (smem <= budget) break;
-        }
-        if (p.stages >= 2 || (ctas == 1 && p.stages == 1)) {
-            *taken = true;
-            break;
-        }
+    int smem = 0;
+    for (p.stages = 8; p.stages >= 1; --p.stages) {
+        smem = p.w_bytes + p.groups * (p.stages * p.stage_bytes + group_fixed(p.r, p.stages));
+        if (smem <= kSmemLimit) break;
     }
+    *taken = p.stages >= 1;
     if (!*taken) return QKN_OK;
-    const int64_t need = (p.T + r.groups - 1) / r.groups, cap = (int64_t)ctas * sm_count();
-    *grid = (int)(need < cap ? need : cap);
+    *grid = (int)(p.T < sm_count() ? p.T : sm_count());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)*grid, 1, 1);
     cfg.blockDim = dim3((unsigned)r.threads, 1, 1);
@@ -649,17 +688,17 @@ qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bo
     return check_launch("rotary_unit_kernel launch");
 }
 
-template <typename TA, typename TW, int MODE, int UPT, bool WIDE>
+template <typename TA, int MODE, int UPT, bool MIXED>
 qkn_status launch_layout(Params &p, const Plan &r, int layout, int *grid, cudaStream_t s, bool *taken) {
-    return layout == QKN_ROTARY_HALF ? launch_kernel<TA, TW, MODE, UPT, true, WIDE>(p, r, grid, s, taken)
-                                     : launch_kernel<TA, TW, MODE, UPT, false, WIDE>(p, r, grid, s, taken);
+    return layout == QKN_ROTARY_HALF ? launch_kernel<TA, MODE, UPT, true, MIXED>(p, r, grid, s, taken)
+                                     : launch_kernel<TA, MODE, UPT, false, MIXED>(p, r, grid, s, taken);
 }
 
 // Launches the unit kernel when it takes the call (*taken); *grid is its number of blocks.
 template <typename TA, typename TW, int MODE>
 qkn_status launch(const Args &a, bool *taken, int *grid, cudaStream_t s) {
     Params p{};
-    const Plan r = plan<TA, TW, MODE>(a, p);
+    const Plan r = plan<TA, MODE>(a, p, sizeof(TW));
     *taken = r.fits;
     if (!r.fits) return QKN_OK;
     p.njobs = a.njobs;
@@ -676,14 +715,13 @@ qkn_status launch(const Args &a, bool *taken, int *grid, cudaStream_t s) {
     p.warps0 = r.warps0;
     p.groups = r.groups;
     p.wait_ns = kWaitTimeoutNs;
-    p.w_bytes = MODE == kRotate ? 0 : ((p.job[0].d + p.job[1].d) * (int)sizeof(TW) + 15) / 16 * 16;
+    p.w_bf16 = sizeof(TW) == 2;
+    p.w_bytes = (MODE == kRotate ? 0 : (p.job[0].d + p.job[1].d) * 4) + 16;  // 16 bytes of zeros
     constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
-    if (r.upt < kUsual) return launch_layout<TA, TW, MODE, kUsual / 2, false>(p, r, a.layout, grid, s, taken);
-    if (r.upt == kUsual)
-        return r.wide ? launch_layout<TA, TW, MODE, kUsual, true>(p, r, a.layout, grid, s, taken)
-                      : launch_layout<TA, TW, MODE, kUsual, false>(p, r, a.layout, grid, s, taken);
+    if (r.mixed) return launch_layout<TA, MODE, kUsual, true>(p, r, a.layout, grid, s, taken);
+    if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, false>(p, r, a.layout, grid, s, taken);
     if constexpr (MODE != kNormBack && kUsual < 4)
-        return launch_layout<TA, TW, MODE, 4, true>(p, r, a.layout, grid, s, taken);
+        return launch_layout<TA, MODE, 4, false>(p, r, a.layout, grid, s, taken);
     return fail(QKN_ERR_UNSUPPORTED, "rotary_unit_kernel: no variant for these rows");
 }
 
