@@ -601,32 +601,31 @@ class _AllocOn:
         return False
 
 
-LAYOUTS = {"half": 0, "interleaved": 1}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_POS_BITS = {torch.int64: 64, torch.int32: 32}
+_NO_ROTARY = (0, None, 64, None, 0, 0)
 
 
-def _rotary_args(positions, inv_freq, head_dim: int, layout: str, T: int, optional: bool):
+def _rotary_args(positions, inv_freq, head_dim: int, layout: str, T: int):
     """(head_dim, positions pointer, pos_bits, inv_freq pointer, rotary_dim, layout code) of a call."""
-    if layout not in LAYOUTS:
+    lay = _LAYOUTS.get(layout)
+    if lay is None:
         raise ValueError(f"layout must be 'half' or 'interleaved', not {layout!r}")
-    if inv_freq is None:
-        if not optional:
-            raise ValueError("inv_freq is required")
-        return 0, None, 64, None, 0, LAYOUTS[layout]
     _cuda(inv_freq, "inv_freq")
     if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous 1-D float64 tensor")
     if positions is None:
         raise ValueError("positions is required with inv_freq")
     _vec(positions, "positions", T)
-    if positions.dtype not in (torch.int32, torch.int64):
+    bits = _POS_BITS.get(positions.dtype)
+    if bits is None:
         raise TypeError("positions must be int32 or int64")
-    return (int(head_dim), positions.data_ptr(), 64 if positions.dtype == torch.int64 else 32, inv_freq.data_ptr(),
-            2 * inv_freq.shape[0], LAYOUTS[layout])
+    return int(head_dim), positions.data_ptr(), bits, inv_freq.data_ptr(), 2 * inv_freq.shape[0], lay
 
 
-def _rows_like(t: torch.Tensor, name: str, q: torch.Tensor):
+def _rows_like(t: torch.Tensor, name: str, q: torch.Tensor, T: int):
     rows, d, ld = _rows(t, name)
-    if rows != q.shape[0] or t.dtype != q.dtype:
+    if rows != T or t.dtype != q.dtype:
         raise ValueError(f"{name} must have q's row count and dtype")
     return d, ld
 
@@ -642,23 +641,39 @@ def _pair_weights(wq, wk, dq: int, dk: int, has_k: bool) -> int:
     return _dtype_code(wq.dtype)
 
 
-def _row_outputs(q, k, q_out, k_out, dk: int, inplace: bool, stream):
+def _result(t: torch.Tensor, given: torch.Tensor | None, name: str, stream):
+    """The output that takes the rows of t, its pointer and pitch: the one given, or a new contiguous one."""
+    if given is None:
+        if stream is None:
+            given = torch.empty_like(t, memory_format=torch.contiguous_format)
+        else:
+            with _AllocOn(stream, t.device):
+                given = torch.empty_like(t, memory_format=torch.contiguous_format)
+        return given, given.data_ptr(), t.shape[1]
+    rows, d = t.shape
+    _out2d(given, name, rows, d, t.dtype)
+    return given, given.data_ptr(), max(given.stride(0), d)
+
+
+def _row_outputs(q, k, q_out, k_out, inplace: bool, stream):
     """Output tensors of a call on q and k, their pointers (None in place) and pitches."""
     if inplace:
         if q_out is not None or k_out is not None:
             raise ValueError("inplace=True takes no q_out or k_out")
-        return q, k, None, None, 0, 0
-    T, dq = q.shape
-    with _AllocOn(stream, q.device):
-        if q_out is None:
-            q_out = torch.empty((T, dq), dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty((T, dk), dtype=q.dtype, device=q.device)
-    _, _, ldq_o = _rows(_out2d(q_out, "q_out", T, dq, q.dtype), "q_out")
-    if k is None:
-        return q_out, None, q_out.data_ptr(), None, ldq_o, 0
-    _, _, ldk_o = _rows(_out2d(k_out, "k_out", T, dk, q.dtype), "k_out")
-    return q_out, k_out, q_out.data_ptr(), k_out.data_ptr(), ldq_o, ldk_o
+        return q, None, 0, k, None, 0
+    return *_result(q, q_out, "q_out", stream), *(_result(k, k_out, "k_out", stream) if k is not None else (None, None, 0))
+
+
+def _call(fn: str, dev: torch.device, *args, stream) -> None:
+    """lib.fn(*args, stream) with the data's device current."""
+    lib = load_library()
+    if torch.cuda.current_device() == dev.index:
+        st = getattr(lib, fn)(*args, _stream(stream))
+    else:
+        with _On(dev):
+            st = getattr(lib, fn)(*args, _stream(stream))
+    if st != 0:
+        _check(fn, st)
 
 
 def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -676,16 +691,13 @@ def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     in :func:`qknorm_fused`.
     """
     T, dq, ldq = _rows(q, "q")
+    dk, ldk = _rows_like(k, "k", q, T) if k is not None else (0, 0)
     act = _dtype_code(q.dtype)
-    dk, ldk = _rows_like(k, "k", q) if k is not None else (0, 0)
-    D, pos, bits, freq, r, lay = _rotary_args(positions, inv_freq, head_dim, layout, T, False)
-    q_out, k_out, qp, kp, ldq_o, ldk_o = _row_outputs(q, k, q_out, k_out, dk, inplace, stream)
+    rot = _rotary_args(positions, inv_freq, head_dim, layout, T)
+    q_out, qp, ldq_o, k_out, kp, ldk_o = _row_outputs(q, k, q_out, k_out, inplace, stream)
     dev = _device(q, k=k, positions=positions, inv_freq=inv_freq, q_out=q_out, k_out=k_out)
-    with _On(dev):
-        st = load_library().rotary_apply(
-            q.data_ptr(), k.data_ptr() if k is not None else None, qp, kp, T, dq, dk, ldq, ldk, ldq_o, ldk_o, D, pos,
-            bits, freq, r, lay, float(mscale), int(bool(inverse)), act, _stream(stream))
-    _check("rotary_apply", st)
+    _call("rotary_apply", dev, q.data_ptr(), k.data_ptr() if k is not None else None, qp, kp, T, dq, dk, ldq, ldk,
+          ldq_o, ldk_o, *rot, mscale, 1 if inverse else 0, act, stream=stream)
     return q_out, k_out
 
 
@@ -701,19 +713,17 @@ def qknorm_rotary(q: torch.Tensor, k: torch.Tensor | None, wq: torch.Tensor, wk:
     :func:`qknorm_fused` and :func:`rotary_apply`.
     """
     T, dq, ldq = _rows(q, "q")
+    has_k = k is not None
+    dk, ldk = _rows_like(k, "k", q, T) if has_k else (0, 0)
     act = _dtype_code(q.dtype)
-    dk, ldk = _rows_like(k, "k", q) if k is not None else (0, 0)
-    wdt = _pair_weights(wq, wk, dq, dk, k is not None)
-    D, pos, bits, freq, r, lay = _rotary_args(positions, inv_freq, head_dim, layout, T, True)
-    q_out, k_out, qp, kp, ldq_o, ldk_o = _row_outputs(q, k, q_out, k_out, dk, inplace, stream)
-    dev = _device(q, k=k, wq=wq, wk=wk if k is not None else None, positions=positions if r else None,
+    wdt = _pair_weights(wq, wk, dq, dk, has_k)
+    rot = _rotary_args(positions, inv_freq, head_dim, layout, T) if inv_freq is not None else _NO_ROTARY
+    q_out, qp, ldq_o, k_out, kp, ldk_o = _row_outputs(q, k, q_out, k_out, inplace, stream)
+    dev = _device(q, k=k, wq=wq, wk=wk if has_k else None, positions=positions if inv_freq is not None else None,
                   inv_freq=inv_freq, q_out=q_out, k_out=k_out)
-    with _On(dev):
-        st = load_library().qknorm_rotary(
-            q.data_ptr(), k.data_ptr() if k is not None else None, wq.data_ptr(),
-            wk.data_ptr() if k is not None else None, qp, kp, T, dq, dk, ldq, ldk, ldq_o, ldk_o, D, pos, bits, freq,
-            r, lay, float(mscale), act, wdt, float(eps), _stream(stream))
-    _check("qknorm_rotary", st)
+    _call("qknorm_rotary", dev, q.data_ptr(), k.data_ptr() if has_k else None, wq.data_ptr(),
+          wk.data_ptr() if has_k else None, qp, kp, T, dq, dk, ldq, ldk, ldq_o, ldk_o, *rot, mscale, act, wdt, eps,
+          stream=stream)
     return q_out, k_out
 
 
@@ -742,39 +752,34 @@ def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.T
     has_k = k is not None
     if has_k != (gk is not None):
         raise ValueError("gk is given with k, and only with k")
-    dgq, ldgq = _rows_like(gq, "gq", q)
-    dk, ldk = _rows_like(k, "k", q) if has_k else (0, 0)
-    dgk, ldgk = _rows_like(gk, "gk", q) if has_k else (0, 0)
+    dgq, ldgq = _rows_like(gq, "gq", q, T)
+    dk, ldk = _rows_like(k, "k", q, T) if has_k else (0, 0)
+    dgk, ldgk = _rows_like(gk, "gk", q, T) if has_k else (0, 0)
     if dgq != dq or dgk != dk:
         raise ValueError("gq and gk must have the widths of q and k")
     wdt = _pair_weights(wq, wk, dq, dk, has_k)
-    D, pos, bits, freq, r, lay = _rotary_args(positions, inv_freq, head_dim, layout, T, True)
-    dq_t, dk_t, qp, kp, ld_dq, ld_dk = _row_outputs(q, k, dq_out, dk_out, dk, False, stream)
+    rot = _rotary_args(positions, inv_freq, head_dim, layout, T) if inv_freq is not None else _NO_ROTARY
+    dq_t, qp, ld_dq, dk_t, kp, ld_dk = _row_outputs(q, k, dq_out, dk_out, False, stream)
     with _AllocOn(stream, q.device):
         if dwq_out is None:
             dwq_out = torch.empty(dq, dtype=torch.float32, device=q.device)
         if has_k and dwk_out is None:
             dwk_out = torch.empty(dk, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            with _On(q.device):  # the size goes by the device's number of SMs
+                need = load_library().qknorm_rotary_backward_workspace_bytes(T, dq, dk)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     for name, t, n in (("dwq_out", dwq_out, dq), ("dwk_out", dwk_out if has_k else None, dk)):
         if t is not None:
             _vec(t, name, n)
             if t.dtype != torch.float32:
                 raise ValueError(f"{name} must be fp32")
-    if workspace is None:
-        with _On(q.device):  # the size goes by the device's number of SMs
-            need = qknorm_rotary_backward_workspace_bytes(T, dq, dk)
-        with _AllocOn(stream, q.device):
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _cuda(workspace, "workspace")
-    dev = _device(q, gq=gq, k=k, gk=gk, wq=wq, wk=wk if has_k else None, positions=positions if r else None,
-                  inv_freq=inv_freq, dq_out=dq_t, dk_out=dk_t, dwq_out=dwq_out, dwk_out=dwk_out if has_k else None,
-                  workspace=workspace)
-    with _On(dev):
-        st = load_library().qknorm_rotary_backward(
-            gq.data_ptr(), gk.data_ptr() if has_k else None, q.data_ptr(), k.data_ptr() if has_k else None,
-            wq.data_ptr(), wk.data_ptr() if has_k else None, qp, kp, dwq_out.data_ptr(),
-            dwk_out.data_ptr() if has_k else None, T, dq, dk, ldgq, ldgk, ldq, ldk, ld_dq, ld_dk, D, pos, bits, freq,
-            r, lay, float(mscale), act, wdt, float(eps), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(stream))
-    _check("qknorm_rotary_backward", st)
+    dev = _device(q, gq=gq, k=k, gk=gk, wq=wq, wk=wk if has_k else None,
+                  positions=positions if inv_freq is not None else None, inv_freq=inv_freq, dq_out=dq_t, dk_out=dk_t,
+                  dwq_out=dwq_out, dwk_out=dwk_out if has_k else None, workspace=workspace)
+    _call("qknorm_rotary_backward", dev, gq.data_ptr(), gk.data_ptr() if has_k else None, q.data_ptr(),
+          k.data_ptr() if has_k else None, wq.data_ptr(), wk.data_ptr() if has_k else None, qp, kp, dwq_out.data_ptr(),
+          dwk_out.data_ptr() if has_k else None, T, dq, dk, ldgq, ldgk, ldq, ldk, ld_dq, ld_dk, *rot, mscale, act, wdt,
+          eps, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
     return dq_t, dk_t, dwq_out, (dwk_out if has_k else None)
