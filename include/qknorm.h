@@ -452,6 +452,70 @@ QKN_API qkn_status qknorm_rotary_backward(const void *dq_out, const void *dk_out
 /* Bytes of device workspace qknorm_rotary_backward needs (0 for invalid sizes). */
 QKN_API size_t qknorm_rotary_backward_workspace_bytes(int64_t T, int64_t dq, int64_t dk);
 
+/* Activations of linear_fused, of the pre-activation z. */
+typedef enum {
+    QKN_ACT_NONE = 0,      /* z */
+    QKN_ACT_RELU = 1,      /* max(z, 0) */
+    QKN_ACT_SILU = 2,      /* z / (1 + e^-z) */
+    QKN_ACT_GELU = 3,      /* z (1 + erf(z / sqrt 2)) / 2 */
+    QKN_ACT_GELU_TANH = 4  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+} qkn_activation;
+
+/*
+ * linear_fused -- a linear layer with everything around its product in the
+ * product's epilogue:
+ *   z[m][n] = r_m * sum_k x[m][k] W[n][k] + bias[n]     fp32 accumulate
+ *   y[m][n] = act(z[m][n]) + residual[m][n]             one rounding to bf16
+ *
+ * No counterpart in the pages beyond FlashNorm's row scale: these are the
+ * block's other projections (attention output with the residual stream, the
+ * feed-forward's up and down), next to flashnorm_proj.
+ *
+ * x         [M][K] bf16, pitch ldx
+ * W         [N][K] bf16 (K contiguous), pitch ldw
+ * y         [M][N] bf16, pitch ldy; must not overlap x, W or preact
+ * bias      [N] of bias_dt, or NULL
+ * residual  [M][N] bf16, pitch ldr, or NULL; may be y itself (the result is
+ *           then added in place)
+ * inv_rms   [M] fp32 row scale (flashnorm_inv_rms, with W folded by
+ *           flashnorm_fold_weights), or NULL for 1
+ * preact    [M][N] bf16, pitch ldz, receives z for linear_fused_backward, or NULL
+ * M >= 0, N and K multiples of 8; pitches multiples of 8; x, W, y, bias,
+ * residual and preact 16-byte aligned.  One launch, nothing is allocated.
+ * A device-side wait that gives up is reported by qkn_check_device.
+ */
+QKN_API qkn_status linear_fused(const void *x, const void *W, void *y,
+                                int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int64_t ldy,
+                                const void *bias, qkn_dtype bias_dt, qkn_activation act,
+                                const void *residual, int64_t ldr, const float *inv_rms,
+                                void *preact, int64_t ldz, void *stream);
+
+/*
+ * linear_fused_backward -- gradients of linear_fused called without inv_rms:
+ *   dz = dy * act'(preact)   (rounded to bf16 for the products)
+ *   dx = dz W,  dW = dz^T x,  dbias = column sums of the unrounded dz
+ * The residual's gradient is dy itself.
+ *
+ * dy      [M][N] bf16, pitch lddy;  preact [M][N] bf16, pitch ldz (ignored for
+ *         QKN_ACT_NONE);  x, W as in the forward call
+ * dx      [M][K] bf16, pitch lddx;  dW [N][K] bf16, pitch lddw;  dbias [N]
+ *         fp32.  Each may be NULL and is then left out (x is read for dW, W
+ *         for dx).  They must not overlap the inputs.  M == 0 writes zeros to
+ *         dW and dbias
+ * workspace  at least linear_fused_backward_workspace_bytes(M, N, K, act)
+ *         bytes of device scratch, 16-byte aligned, or NULL to allocate it
+ *         stream-ordered inside the call
+ */
+QKN_API qkn_status linear_fused_backward(const void *dy, const void *preact, const void *x, const void *W,
+                                         void *dx, void *dW, float *dbias,
+                                         int64_t M, int64_t N, int64_t K, int64_t lddy, int64_t ldz,
+                                         int64_t ldx, int64_t ldw, int64_t lddx, int64_t lddw,
+                                         qkn_activation act, void *workspace, size_t workspace_bytes,
+                                         void *stream);
+
+/* Bytes of device workspace linear_fused_backward needs (0 for invalid sizes). */
+QKN_API size_t linear_fused_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, qkn_activation act);
+
 /*
  * qkn_check_device -- synchronises `stream`, then reads and clears the
  * current device's error word.  Returns QKN_ERR_TIMEOUT when a bounded

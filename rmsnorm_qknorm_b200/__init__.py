@@ -21,6 +21,8 @@ Entry points (same names as the C ABI):
 * :func:`rotary_apply` -- rotary positions on query and key rows (and back).
 * :func:`qknorm_rotary`, :func:`qknorm_rotary_backward` -- QK-Norm and rotary
   positions in one pass, and the gradients of both.
+* :func:`linear_fused`, :func:`linear_fused_backward` -- a linear layer with
+  bias, activation and residual in its epilogue, and its gradients.
 * :func:`qkv_norm_proj` -- QKV projection + QKV-normalisation with the
   pre-attention RMSNorm eliminated (FlashNorm's scale-invariance identity).
 """
@@ -53,6 +55,9 @@ __all__ = [
     "qknorm_rotary",
     "qknorm_rotary_backward",
     "qknorm_rotary_backward_workspace_bytes",
+    "linear_fused",
+    "linear_fused_backward",
+    "linear_fused_backward_workspace_bytes",
     "STATUS_NAMES",
     "QKN_MAX_SEG",
 ]
@@ -116,10 +121,14 @@ def load_library() -> ctypes.CDLL:
                                                                       p, ctypes.c_size_t, p])
         lib.qknorm_rotary_backward_workspace_bytes.argtypes = [i64, i64, i64]
         lib.qknorm_rotary_backward_workspace_bytes.restype = ctypes.c_size_t
+        lib.linear_fused.argtypes = [p, p, p] + [i64] * 6 + [p, i32, i32, p, i64, p, p, i64, p]
+        lib.linear_fused_backward.argtypes = [p] * 7 + [i64] * 9 + [i32, p, ctypes.c_size_t, p]
+        lib.linear_fused_backward_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        lib.linear_fused_backward_workspace_bytes.restype = ctypes.c_size_t
         lib.qkn_check_device.argtypes = [p]
         for f in ("qknorm_fused", "qknorm_fused_host", "qkv_proj_qknorm", "rmsnorm_partial_stats", "flashnorm_fold_weights",
                   "flashnorm_proj", "flashnorm_inv_rms", "rmsnorm_apply_partials", "qkv_norm_proj", "rotary_apply", "qknorm_rotary",
-                  "qknorm_rotary_backward", "qkn_check_device"):
+                  "qknorm_rotary_backward", "linear_fused", "linear_fused_backward", "qkn_check_device"):
             getattr(lib, f).restype = ctypes.c_int
         lib.qkn_last_error.restype = ctypes.c_char_p
         lib.qkn_last_error.argtypes = []
@@ -783,3 +792,146 @@ def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.T
           dwk_out.data_ptr() if has_k else None, T, dq, dk, ldgq, ldgk, ldq, ldk, ld_dq, ld_dk, *rot, mscale, act, wdt,
           eps, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
     return dq_t, dk_t, dwq_out, (dwk_out if has_k else None)
+
+
+_ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _activation(act: str) -> int:
+    code = _ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(_ACTIVATIONS)}, not {act!r}")
+    return code
+
+
+def _bf16_rows(t: torch.Tensor, name: str):
+    rows, cols, ld = _rows(t, name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bf16")
+    # a single row has no pitch of its own
+    return rows, cols, ld if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _bf16_like(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
+    r, c, ld = _bf16_rows(t, name)
+    if r != rows or c != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}]")
+    return ld
+
+
+def _new(rows: int, cols: int, dtype: torch.dtype, dev: torch.device, stream) -> torch.Tensor:
+    with _AllocOn(stream, dev):
+        return torch.empty((rows, cols), dtype=dtype, device=dev)
+
+
+def linear_fused(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+                 residual: torch.Tensor | None = None, *, inv_rms: torch.Tensor | None = None,
+                 preact_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """y [M, N] = act(r * (x W^T) + bias) + residual, bf16 in and out, fp32 accumulate, one launch.
+
+    x [M, K] and W [N, K] are bf16 (row pitches from their strides, multiples
+    of 8), ``bias`` [N] bf16 or fp32, ``act`` one of "none", "relu", "silu",
+    "gelu" (erf) and "gelu_tanh".  ``residual`` [M, N] may be ``out`` itself.
+    ``inv_rms`` (fp32 [M]) scales the rows of the product: FlashNorm's
+    deferred 1/rms, with W from :func:`flashnorm_fold_weights`.
+    ``preact_out`` receives the pre-activation for :func:`linear_fused_backward`.
+    """
+    M, K, ldx = _bf16_rows(x, "x")
+    N, K2, ldw = _bf16_rows(W, "W")
+    if K2 != K:
+        raise ValueError(f"W has K={K2} but x has K={K}")
+    code = _activation(act)
+    bias_dt = QKN_BF16
+    if bias is not None:
+        _vec(bias, "bias", N)
+        bias_dt = _dtype_code(bias.dtype)
+    ldr = _bf16_like(residual, "residual", M, N) if residual is not None else 0
+    if inv_rms is not None:
+        _vec(inv_rms, "inv_rms", M)
+        if inv_rms.dtype != torch.float32:
+            raise ValueError("inv_rms must be fp32")
+    ldz = _bf16_like(preact_out, "preact_out", M, N) if preact_out is not None else 0
+    if out is None:
+        out, ldy = _new(M, N, torch.bfloat16, x.device, stream), N
+    else:
+        ldy = _bf16_like(out, "out", M, N)
+    dev = _device(x, W=W, bias=bias, residual=residual, inv_rms=inv_rms, preact_out=preact_out, out=out)
+    _call("linear_fused", dev, x.data_ptr(), W.data_ptr(), out.data_ptr(), M, N, K, ldx, ldw, ldy,
+          bias.data_ptr() if bias is not None else None, bias_dt, code,
+          residual.data_ptr() if residual is not None else None, ldr,
+          inv_rms.data_ptr() if inv_rms is not None else None,
+          preact_out.data_ptr() if preact_out is not None else None, ldz, stream=stream)
+    return out
+
+
+def linear_fused_backward_workspace_bytes(M: int, N: int, K: int, act: str = "none") -> int:
+    """Device scratch linear_fused_backward needs for these sizes (bytes)."""
+    return int(load_library().linear_fused_backward_workspace_bytes(M, N, K, _activation(act)))
+
+
+def linear_fused_backward(dy: torch.Tensor, x: torch.Tensor | None, W: torch.Tensor | None,
+                          preact: torch.Tensor | None = None, act: str = "none", *, need_dbias: bool = False,
+                          dx_out: torch.Tensor | None = None, dW_out: torch.Tensor | None = None,
+                          dbias_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients ``(dx, dW, dbias)`` of :func:`linear_fused` (called without ``inv_rms``) for dy [M, N].
+
+    dx needs W and dW needs x: the one whose input is None is left out.
+    dbias (fp32 [N]) is formed with ``need_dbias`` or ``dbias_out``.
+    ``preact`` is what the forward call wrote to ``preact_out`` (not needed
+    for act "none").  The residual's gradient is dy itself.  ``workspace``
+    (uint8 CUDA tensor of at least ``linear_fused_backward_workspace_bytes``)
+    avoids an allocation inside the call.
+    """
+    M, N, lddy = _bf16_rows(dy, "dy")
+    code = _activation(act)
+    if x is None and W is None and not need_dbias and dbias_out is None:
+        raise ValueError("nothing to compute: x, W, need_dbias and dbias_out are all absent")
+    K = 8
+    if W is not None:
+        n, K, ldw = _bf16_rows(W, "W")
+        if n != N:
+            raise ValueError(f"W has {n} rows but dy has {N} columns")
+    if x is not None:
+        m, kx, ldx = _bf16_rows(x, "x")
+        if m != M or (W is not None and kx != K):
+            raise ValueError("x must be [M, K]")
+        K = kx
+    if code != 0 and preact is None:
+        raise ValueError("preact is required with an activation")
+    if code == 0:
+        preact = None
+    ldz = _bf16_like(preact, "preact", M, N) if preact is not None else 0
+    lddx = lddw = 0
+    if W is not None:
+        if dx_out is None:
+            dx_out, lddx = _new(M, K, torch.bfloat16, dy.device, stream), K
+        else:
+            lddx = _bf16_like(dx_out, "dx_out", M, K)
+    elif dx_out is not None:
+        raise ValueError("dx_out needs W")
+    if x is not None:
+        if dW_out is None:
+            dW_out, lddw = _new(N, K, torch.bfloat16, dy.device, stream), K
+        else:
+            lddw = _bf16_like(dW_out, "dW_out", N, K)
+    elif dW_out is not None:
+        raise ValueError("dW_out needs x")
+    with _AllocOn(stream, dy.device):
+        if need_dbias and dbias_out is None:
+            dbias_out = torch.empty(N, dtype=torch.float32, device=dy.device)
+        if workspace is None:
+            with _On(dy.device):  # the size goes by the device's number of SMs
+                need = load_library().linear_fused_backward_workspace_bytes(M, N, K, code)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dy.device)
+    _cuda(workspace, "workspace")
+    if dbias_out is not None:
+        _vec(dbias_out, "dbias_out", N)
+        if dbias_out.dtype != torch.float32:
+            raise ValueError("dbias_out must be fp32")
+    dev = _device(dy, x=x, W=W, preact=preact, dx_out=dx_out, dW_out=dW_out, dbias_out=dbias_out, workspace=workspace)
+    ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    _call("linear_fused_backward", dev, dy.data_ptr(), ptr(preact), ptr(x), ptr(W), ptr(dx_out), ptr(dW_out),
+          ptr(dbias_out), M, N, K, lddy, ldz, ldx if x is not None else 0, ldw if W is not None else 0, lddx, lddw, code,
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+    return dx_out, dW_out, dbias_out

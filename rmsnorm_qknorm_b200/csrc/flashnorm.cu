@@ -557,6 +557,22 @@ qkn_status make_tmap_store(CUtensorMap *m, void *ptr, int64_t rows, int64_t cols
     return QKN_OK;
 }
 
+qkn_status make_tmap_pitched(CUtensorMap *m, const void *ptr, int64_t rows, int64_t inner, int64_t pitch,
+                             int box_inner, int box_rows, int swizzle_bytes) {
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return fail(QKN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+    cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(pitch * 2)};
+    cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(QKN_ERR_CUDA, "cuTensorMapEncodeTiled (pitched) failed (CUresult %d)", (int)r);
+    return QKN_OK;
+}
+
 qkn_status launch_inv_rms(const void *x, float *inv, int64_t M, int64_t K, float eps, cudaStream_t s) {
     const int64_t blocks = (M + 7) / 8;
     if (blocks > 0x7fffffffLL) return fail(QKN_ERR_SHAPE, "flashnorm_proj: M too large");
@@ -753,13 +769,15 @@ extern "C" QKN_API qkn_status qkn_check_device(void *stream) {
         const int zero = 0;
         cudaMemcpyToSymbol(g_device_error, &zero, sizeof zero);
     }
-    int norm_flag = 0, qkv_flag = 0, rotary_flag = 0;
+    int norm_flag = 0, qkv_flag = 0, rotary_flag = 0, linear_flag = 0;
     if (qkn_status st = read_norm_error(&norm_flag)) return st;
     if (qkn_status st = read_qkv_error(&qkv_flag)) return st;
     if (qkn_status st = read_rotary_error(&rotary_flag)) return st;
-    if (flag != 0 || norm_flag != 0 || qkv_flag != 0 || rotary_flag != 0)
-        return fail(QKN_ERR_TIMEOUT, "a bounded device-side wait gave up (projection %d, norm %d, fused QKV %d, rotary %d)",
-                    flag, norm_flag, qkv_flag, rotary_flag);
+    if (qkn_status st = read_linear_error(&linear_flag)) return st;
+    if (flag != 0 || norm_flag != 0 || qkv_flag != 0 || rotary_flag != 0 || linear_flag != 0)
+        return fail(QKN_ERR_TIMEOUT,
+                    "a bounded device-side wait gave up (projection %d, norm %d, fused QKV %d, rotary %d, linear %d)",
+                    flag, norm_flag, qkv_flag, rotary_flag, linear_flag);
     return QKN_OK;
 }
 

@@ -86,6 +86,11 @@ qkn_status make_tmap(CUtensorMap *m, const void *ptr, int64_t rows, int64_t inne
 // position j ^ ((r >> 1) & 3)); parts of a box outside the tensor are skipped.
 qkn_status make_tmap_store(CUtensorMap *m, void *ptr, int64_t rows, int64_t cols);
 
+// 2-D bf16 tensor [rows][inner], rows `pitch` elements apart, as a TMA tensor
+// map of box_inner x box_rows boxes with a 64- or 128-byte swizzle.
+qkn_status make_tmap_pitched(CUtensorMap *m, const void *ptr, int64_t rows, int64_t inner, int64_t pitch,
+                             int box_inner, int box_rows, int swizzle_bytes);
+
 // inv[m] = 1/sqrt(sum_k x[m][k]^2 / K + eps) for bf16 x [M][K] (K a multiple
 // of 8, rows 16-byte aligned), on stream s.
 qkn_status launch_inv_rms(const void *x, float *inv, int64_t M, int64_t K, float eps, cudaStream_t s);
@@ -95,5 +100,8 @@ qkn_status read_qkv_error(int *flag);
 
 // Reads (and clears) the device error word of the rotary unit kernel.
 qkn_status read_rotary_error(int *flag);
+
+// Reads (and clears) the device error word of the fused linear layer's kernels.
+qkn_status read_linear_error(int *flag);
 
 }  // namespace qkn

@@ -1,0 +1,251 @@
+// Fused linear layer: y = act(r (x W^T) + b) + residual, and its gradients.
+//
+//   z = r_m sum_k x[m][k] W[n][k] + b[n],  y = act(z) + residual
+//   dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum_m dz
+// The products run on the tensor cores (linear_pair.cuh) with everything else
+// in their epilogue; dz is formed once (and rounded to bf16, the products'
+// operand type) by an element-wise pass that adds up db in fp32 on the way.
+#include <atomic>
+#include <cuda.h>
+#include <math.h>
+
+#include "gemm_tc.cuh"
+#include "linear_math.cuh"
+#include "pair_tc.cuh"
+#include "qkn_common.cuh"
+#include "qkn_sync.cuh"
+
+namespace qkn {
+
+// Set by a bounded wait of the linear kernels that gave up (see qkn_check_device).
+__device__ int g_linear_error = 0;
+
+#include "linear_pair.cuh"
+
+namespace lin {
+
+// ---------------------------------------------------------------- dz and db
+
+// dz = dy act'(z) and the partial column sums of dz: a block walks the rows of
+// its slice over 256 columns, 8 rows at a time, a 16-byte chunk per thread;
+// the eight rows' sums meet in shared memory in row order.
+constexpr int kDzCols = 256, kDzThreads = 256;
+
+__global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const __nv_bfloat16 *__restrict__ dy,
+                                                               const __nv_bfloat16 *__restrict__ z,
+                                                               __nv_bfloat16 *__restrict__ dz, float *__restrict__ part,
+                                                               int64_t M, int N, int64_t lddy, int64_t ldz, int act,
+                                                               int slices) {
+    __shared__ float red[8][kDzCols + 4];
+    const int chunk = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int col = blockIdx.x * kDzCols + chunk * 8;
+    const bool in = col < N;
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+    for (int64_t row = (int64_t)blockIdx.y * 8 + rl; in && row < M; row += (int64_t)slices * 8) {
+        float f[8];
+        Chunk<__nv_bfloat16>::unpack(ld_stream(dy + row * lddy + col), f);
+        if (act != QKN_ACT_NONE) {
+            float v[8];
+            Chunk<__nv_bfloat16>::unpack(ld_stream(z + row * ldz + col), v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= slope(act, v[e]);
+            *reinterpret_cast<uint4 *>(dz + row * N + col) = Chunk<__nv_bfloat16>::pack(f);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += f[e];
+    }
+    if (part == nullptr) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[rl][chunk * 8 + e] = sum[e];
+    __syncthreads();
+    const int c = blockIdx.x * kDzCols + threadIdx.x;
+    if (c < N) {
+        float s = red[0][threadIdx.x];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) s += red[j][threadIdx.x];
+        part[(int64_t)blockIdx.y * N + c] = s;
+    }
+}
+
+// db[c] = sum over slices of part[slice][c], in a fixed order.
+__global__ void __launch_bounds__(256) linear_db_kernel(const float *__restrict__ part, float *__restrict__ db, int N,
+                                                        int slices) {
+    __shared__ float red[8][33];
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+    float s = 0.f;
+    if (col < N)
+        for (int i = k; i < slices; i += 8) s += part[(int64_t)i * N + col];
+    red[k][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (k == 0 && col < N) {
+        float v = red[0][threadIdx.x];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) v += red[j][threadIdx.x];
+        db[col] = v;
+    }
+}
+
+// Row slices of the pass: eight 256-thread blocks per SM in all, at least a row group each.
+int dz_slices(int64_t M, int64_t N) {
+    const int64_t cols = (N + kDzCols - 1) / kDzCols, groups = (M + 7) / 8;
+    int64_t s = 8 * (int64_t)sm_count() / cols;
+    if (s < 1) s = 1;
+    if (s > groups) s = groups;
+    return (int)s;
+}
+
+size_t dz_bytes(int64_t M, int64_t N, int act) {
+    return act == QKN_ACT_NONE ? 0 : ((size_t)M * (size_t)N * 2 + 255) / 256 * 256;
+}
+
+template <int ACT>
+qkn_status forward(const pair::Matrix &x, const pair::Matrix &W, const pair::Matrix &y, const pair::Matrix *res,
+                   const pair::Matrix *z, const Epilogue &epi, int64_t K, cudaStream_t s) {
+    return pair::launch<false, false, ACT>(x, W, y, res, z, epi, K, s);
+}
+
+bool pitch_ok(int64_t ld, int64_t width) { return ld >= width && ld % 8 == 0; }
+
+}  // namespace lin
+
+qkn_status read_linear_error(int *flag) {
+    cudaError_t e = cudaMemcpyFromSymbol(flag, g_linear_error, sizeof(int));
+    if (e != cudaSuccess) return cuda_fail(e, "reading the linear kernels' device error word");
+    if (*flag) {
+        const int zero = 0;
+        cudaMemcpyToSymbol(g_linear_error, &zero, sizeof zero);
+    }
+    return QKN_OK;
+}
+
+}  // namespace qkn
+
+using namespace qkn;
+
+extern "C" QKN_API qkn_status linear_fused(const void *x, const void *W, void *y, int64_t M, int64_t N, int64_t K,
+                                           int64_t ldx, int64_t ldw, int64_t ldy, const void *bias, qkn_dtype bias_dt,
+                                           qkn_activation act, const void *residual, int64_t ldr, const float *inv_rms,
+                                           void *preact, int64_t ldz, void *stream) {
+    const char *fn = "linear_fused";
+    if (M < 0 || N < 1 || K < 1 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL)
+        return fail(QKN_ERR_SHAPE, "%s: bad sizes M=%lld N=%lld K=%lld", fn, (long long)M, (long long)N, (long long)K);
+    if (K % 8 != 0 || N % 8 != 0)
+        return fail(QKN_ERR_SHAPE, "%s: K=%lld and N=%lld must be multiples of 8", fn, (long long)K, (long long)N);
+    if (!lin::pitch_ok(ldx, K) || !lin::pitch_ok(ldw, K) || !lin::pitch_ok(ldy, N) ||
+        (residual && !lin::pitch_ok(ldr, N)) || (preact && !lin::pitch_ok(ldz, N)))
+        return fail(QKN_ERR_SHAPE, "%s: leading dimensions must be multiples of 8 and at least the row width", fn);
+    if (bias && !valid_dtype(bias_dt)) return fail(QKN_ERR_DTYPE, "%s: unknown bias dtype %d", fn, (int)bias_dt);
+    if ((int)act < QKN_ACT_NONE || (int)act > QKN_ACT_GELU_TANH)
+        return fail(QKN_ERR_UNSUPPORTED, "%s: unknown activation %d", fn, (int)act);
+    if (M == 0) return QKN_OK;
+    if (x == nullptr || W == nullptr || y == nullptr) return fail(QKN_ERR_NULL, "%s: x, W and y are required", fn);
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(y, 16) || !aligned(bias, 16) || !aligned(residual, 16) ||
+        !aligned(preact, 16) || !aligned(inv_rms, 4))
+        return fail(QKN_ERR_ALIGN, "%s: x, W, y, bias, residual and preact must be 16-byte aligned", fn);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const lin::pair::Matrix mx = {x, M, K, ldx}, mw = {W, N, K, ldw}, my = {y, M, N, ldy}, mr = {residual, M, N, ldr},
+                            mz = {preact, M, N, ldz};
+    const lin::pair::Matrix *res = residual ? &mr : nullptr, *z = preact ? &mz : nullptr;
+    lin::Epilogue e{};
+    e.inv_rms = inv_rms;
+    e.bias = bias;
+    e.bias_bf16 = bias_dt == QKN_BF16;
+    switch (act) {
+    case QKN_ACT_RELU: return lin::forward<QKN_ACT_RELU>(mx, mw, my, res, z, e, K, s);
+    case QKN_ACT_SILU: return lin::forward<QKN_ACT_SILU>(mx, mw, my, res, z, e, K, s);
+    case QKN_ACT_GELU: return lin::forward<QKN_ACT_GELU>(mx, mw, my, res, z, e, K, s);
+    case QKN_ACT_GELU_TANH: return lin::forward<QKN_ACT_GELU_TANH>(mx, mw, my, res, z, e, K, s);
+    default: return lin::forward<QKN_ACT_NONE>(mx, mw, my, res, z, e, K, s);
+    }
+}
+
+extern "C" QKN_API size_t linear_fused_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, qkn_activation act) {
+    if (M < 0 || N < 1 || K < 1 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL || (int)act < QKN_ACT_NONE ||
+        (int)act > QKN_ACT_GELU_TANH)
+        return 0;
+    return lin::dz_bytes(M, N, act) + (M ? (size_t)lin::dz_slices(M, N) * (size_t)N * 4 : 0) + 16;
+}
+
+extern "C" QKN_API qkn_status linear_fused_backward(const void *dy, const void *preact, const void *x, const void *W,
+                                                    void *dx, void *dW, float *dbias, int64_t M, int64_t N, int64_t K,
+                                                    int64_t lddy, int64_t ldz, int64_t ldx, int64_t ldw, int64_t lddx,
+                                                    int64_t lddw, qkn_activation act, void *workspace,
+                                                    size_t workspace_bytes, void *stream) {
+    const char *fn = "linear_fused_backward";
+    if (M < 0 || N < 1 || K < 1 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL)
+        return fail(QKN_ERR_SHAPE, "%s: bad sizes M=%lld N=%lld K=%lld", fn, (long long)M, (long long)N, (long long)K);
+    if (K % 8 != 0 || N % 8 != 0)
+        return fail(QKN_ERR_SHAPE, "%s: K=%lld and N=%lld must be multiples of 8", fn, (long long)K, (long long)N);
+    if ((int)act < QKN_ACT_NONE || (int)act > QKN_ACT_GELU_TANH)
+        return fail(QKN_ERR_UNSUPPORTED, "%s: unknown activation %d", fn, (int)act);
+    const bool has_z = act != QKN_ACT_NONE;
+    if (!lin::pitch_ok(lddy, N) || (has_z && !lin::pitch_ok(ldz, N)) || (dW && !lin::pitch_ok(ldx, K)) ||
+        (dx && !lin::pitch_ok(ldw, K)) || (dx && !lin::pitch_ok(lddx, K)) || (dW && !lin::pitch_ok(lddw, K)))
+        return fail(QKN_ERR_SHAPE, "%s: leading dimensions must be multiples of 8 and at least the row width", fn);
+    if (dx == nullptr && dW == nullptr && dbias == nullptr) return QKN_OK;
+    if (M > 0) {
+        if (dy == nullptr || (has_z && preact == nullptr) || (dW && x == nullptr) || (dx && W == nullptr))
+            return fail(QKN_ERR_NULL, "%s: dy, preact (with an activation), x (for dW) and W (for dx) are required", fn);
+        if (!aligned(dy, 16) || !aligned(preact, 16) || !aligned(x, 16) || !aligned(W, 16) || !aligned(dx, 16))
+            return fail(QKN_ERR_ALIGN, "%s: dy, preact, x, W and dx must be 16-byte aligned", fn);
+    }
+    if (!aligned(dW, 16) || !aligned(dbias, 4))
+        return fail(QKN_ERR_ALIGN, "%s: dW must be 16-byte aligned, dbias 4-byte aligned", fn);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t need = linear_fused_backward_workspace_bytes(M, N, K, act);
+    if (workspace != nullptr) {
+        if (workspace_bytes < need)
+            return fail(QKN_ERR_SHAPE, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+        if (!aligned(workspace, 16)) return fail(QKN_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+    }
+    if (M == 0) {  // no rows: the gradients of W and b are empty sums
+        cudaError_t e = cudaSuccess;
+        if (dW != nullptr) e = cudaMemset2DAsync(dW, (size_t)lddw * 2, 0, (size_t)K * 2, (size_t)N, s);
+        if (e == cudaSuccess && dbias != nullptr) e = cudaMemsetAsync(dbias, 0, (size_t)N * 4, s);
+        return e == cudaSuccess ? QKN_OK : cuda_fail(e, "linear_fused_backward: clearing the gradients");
+    }
+    void *own = nullptr;
+    if (workspace == nullptr && (has_z || dbias != nullptr)) {
+        const cudaError_t e = cudaMallocAsync(&own, need, s);
+        if (e != cudaSuccess) return cuda_fail(e, "linear_fused_backward: workspace");
+        workspace = own;
+    }
+    const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(dy);
+    int64_t ldg = lddy;
+    qkn_status st = QKN_OK;
+    if (has_z || dbias != nullptr) {
+        __nv_bfloat16 *dz = static_cast<__nv_bfloat16 *>(workspace);
+        float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + lin::dz_bytes(M, N, act));
+        const int slices = lin::dz_slices(M, N);
+        const dim3 grid((unsigned)((N + lin::kDzCols - 1) / lin::kDzCols), (unsigned)slices);
+        lin::linear_dz_kernel<<<grid, lin::kDzThreads, 0, s>>>(g, static_cast<const __nv_bfloat16 *>(preact), dz,
+                                                               dbias != nullptr ? part : nullptr, M, (int)N, lddy, ldz,
+                                                               (int)act, slices);
+        st = check_launch("linear_dz_kernel launch");
+        if (st == QKN_OK && dbias != nullptr) {
+            lin::linear_db_kernel<<<(unsigned)((N + 31) / 32), 256, 0, s>>>(part, dbias, (int)N, slices);
+            st = check_launch("linear_db_kernel launch");
+        }
+        if (has_z) {
+            g = dz;
+            ldg = N;
+        }
+    }
+    const lin::pair::Matrix mg = {g, M, N, ldg}, mx = {x, M, K, ldx}, mw = {W, N, K, ldw};
+    const lin::Epilogue e{};
+    if (st == QKN_OK && dx != nullptr) {
+        const lin::pair::Matrix out = {dx, M, K, lddx};
+        st = lin::pair::launch<false, true, QKN_ACT_NONE>(mg, mw, out, nullptr, nullptr, e, N, s);
+    }
+    if (st == QKN_OK && dW != nullptr) {
+        const lin::pair::Matrix out = {dW, N, K, lddw};
+        st = lin::pair::launch<true, true, QKN_ACT_NONE>(mg, mx, out, nullptr, nullptr, e, M, s);
+    }
+    if (own != nullptr) {
+        const cudaError_t f = cudaFreeAsync(own, s);
+        if (f != cudaSuccess && st == QKN_OK) st = cuda_fail(f, "linear_fused_backward: releasing the workspace");
+    }
+    return st;
+}
