@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cuda.h>
 #include <math.h>
+#include <stdlib.h>
 
 #include "gemm_tc.cuh"
 #include "linear_math.cuh"
@@ -21,6 +22,7 @@ namespace qkn {
 __device__ int g_linear_error = 0;
 
 #include "linear_pair.cuh"
+#include "linear_rows.cuh"
 
 namespace lin {
 
@@ -100,9 +102,14 @@ size_t dz_bytes(int64_t M, int64_t N, int act) {
     return act == QKN_ACT_NONE ? 0 : ((size_t)M * (size_t)N * 2 + 255) / 256 * 256;
 }
 
+constexpr int kRowsMax = 128;
+
 template <int ACT>
 qkn_status forward(const pair::Matrix &x, const pair::Matrix &W, const pair::Matrix &y, const pair::Matrix *res,
                    const pair::Matrix *z, const Epilogue &epi, int64_t K, cudaStream_t s) {
+    int limit = kRowsMax;
+    if (const char *v = getenv("LIN_ROWS_MAX")) limit = atoi(v);
+    if (y.rows <= limit) return rows::launch<ACT>(x, W, y, res, z, epi, K, s);
     return pair::launch<false, false, ACT>(x, W, y, res, z, epi, K, s);
 }
 

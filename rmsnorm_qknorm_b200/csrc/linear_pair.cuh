@@ -10,14 +10,16 @@
 // of each operand per CTA, as 128-byte-swizzled rows of 64 k, or as two
 // blocks of 64 (k) rows of 64 m.
 //
-// Roles per CTA (192 threads) as in the FlashNorm projection: warp 0 moves
-// tiles with TMA, one lane of the even CTA's warp 1 issues the MMAs, warps
-// 2-5 run the epilogue of a tile while the MMAs of the next one run into the
-// other accumulator.  The epilogue works on 32 x 32 blocks: accumulator
-// -> times the row's scale, plus bias -> z (stored where asked) -> activation
-// -> plus residual -> y.  A residual block is brought by TMA into the buffer
-// that y leaves from, one block ahead, and each thread overwrites the bytes
-// it read.
+// Roles per CTA (320 threads): warp 0 moves tiles with TMA, one lane of the
+// even CTA's warp 1 issues the MMAs, warps 2-9 run the epilogue of a tile
+// while the MMAs of the next one run into the other accumulator: a quarter of
+// the rows and half of the columns per warp, a row per thread, 32 columns at
+// a time: accumulator -> times the row's scale, plus bias -> z (stored where
+// asked) -> activation -> plus residual -> y.  Residual, z and y are read and
+// written where they lie, whole 32-byte sectors per thread (16 bytes where
+// the rows are not 32-byte aligned); the residual is asked for before the
+// accumulator is waited for.  (Staged through shared memory and TMA by four
+// warps, a block was a chain of waits: 27 us for a call of one tile.)
 // Every wait is bounded and records a failure in g_linear_error.
 #pragma once
 
@@ -25,21 +27,24 @@ namespace lin {
 namespace pair {
 
 constexpr int BM = 128, BN = 256, BN_CTA = 128, BK = 64;
-constexpr int STAGES = 6;
+constexpr int STAGES = 7;
 constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN_CTA * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int PAIR_STAGE_BYTES = 2 * STAGE_BYTES;
 constexpr int ACC_COLS = BN, TMEM_COLS = 2 * ACC_COLS;
-constexpr int THREADS = 192;
-constexpr int BLOCK_BYTES = 2048;                  // a 32 x 32 bf16 block
-constexpr int EPI_BYTES = 4 * 4 * BLOCK_BYTES;     // per epilogue warp: two blocks of y (residual first), two of z
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int BAR_BYTES = 256;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES + 1024;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BAR_BYTES + 1024;
 constexpr int GROUP_M = 16;  // pair row blocks walked together down each column block (operands shared in L2)
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
 struct Args {
     Epilogue epi;
+    const __nv_bfloat16 *res;
+    __nv_bfloat16 *y, *z;
+    int64_t ldr, ldy, ldz;
+    int wide;              // residual, z and y rows are 32-byte aligned
     int M, N;              // of C
     int pm_blocks, n_blocks, k_blocks, num_tiles;
 };
@@ -97,19 +102,51 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *ma
     }
 }
 
+// 16 bf16 of a row, as far as they lie inside it: 32 bytes at once where the rows allow.
+__device__ __forceinline__ void load16(const __nv_bfloat16 *p, bool wide, int left, uint32_t (&w)[8]) {
+    if (wide && left >= 16) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p) : "memory");
+        return;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (left > 8 * h) v = *reinterpret_cast<const uint4 *>(p + 8 * h);
+        w[4 * h] = v.x;
+        w[4 * h + 1] = v.y;
+        w[4 * h + 2] = v.z;
+        w[4 * h + 3] = v.w;
+    }
+}
+
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, bool wide, int left, const float (&f)[16]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    if (wide && left >= 16) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+        return;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (left > 8 * h) *reinterpret_cast<uint4 *>(p + 8 * h) = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+}
+
 template <bool A_MN, bool B_MN, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                   const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ CUtensorMap tmap_res,
-                   const __grid_constant__ CUtensorMap tmap_z, const Args g) {
+                   const Args g) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES + EPI_BYTES);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES);
     uint64_t *full = bars, *empty = bars + STAGES;
     uint64_t *acc_full = bars + 2 * STAGES, *acc_empty = bars + 2 * STAGES + 2;
     uint64_t *drained = bars + 2 * STAGES + 4;
-    uint64_t *res_full = bars + 2 * STAGES + 5;  // [4 warps][2]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 13);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 5);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -123,10 +160,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&acc_full[a]), 1);   // the even CTA's commit
-            mbar_init(smem_u32(&acc_empty[a]), 8);  // even CTA: four epilogue warps of each CTA
+            mbar_init(smem_u32(&acc_empty[a]), 2 * EPI_WARPS);  // even CTA: the epilogue warps of both
         }
         mbar_init(smem_u32(drained), 1);
-        for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&res_full[i]), 1);
         mbar_init_fence();
     }
     if (warp == 1) {  // whole warp, in both CTAs: the pair's tensor memory
@@ -138,6 +174,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy
     gemm::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    // the previous kernel on the stream has finished before any global memory is touched
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer (both CTAs)
@@ -210,109 +249,68 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
         }
         __syncwarp();
     } else {
-        // ---------------------------------------------------------------- epilogue (warps 2..5, both CTAs)
-        const int quarter = warp & 3;  // TMEM lanes this warp may access: 32 * quarter ...
-        const uint32_t ybuf = smem_u32(smem + STAGES * STAGE_BYTES) + (uint32_t)quarter * 4u * BLOCK_BYTES;
-        const uint32_t zbuf = ybuf + 2u * BLOCK_BYTES;
-        const uint32_t rbar = smem_u32(&res_full[2 * quarter]);
+        // ---------------------------------------------------------------- epilogue (warps 2..9, both CTAs)
+        const int quarter = warp & 3;       // TMEM lanes this warp may access: 32 * quarter ...
+        const int half = (warp - 2) >> 2;   // its half of the columns
         const uint32_t acc_empty_leader0 = map_to_rank(smem_u32(&acc_empty[0]), 0);
-        const bool has_res = g.epi.has_res != 0, has_z = g.epi.has_z != 0;
-        uint32_t blk = 0, res_issued = 0, res_taken = 0;  // blocks so far; residual blocks asked for, arrived
-        bool ok = true;
+        const bool wide = g.wide != 0;
         int it = 0;
-        // lane 0: the residual block at (col, row) into the y buffer of the res_issued-th block,
-        // once the stores issued so far have read their buffers
-        auto fetch = [&](int col, int row) {
-            bulk_wait_read0();
-            const uint32_t bar = rbar + (res_issued & 1u) * 8u;
-            mbar_arrive_expect_tx(bar, BLOCK_BYTES);
-            tma_load_2d(ybuf + (res_issued & 1u) * BLOCK_BYTES, &tmap_res, col, row, bar);
-        };
-        for (int tile = pair_id; ok && tile < g.num_tiles; tile += num_pairs, ++it) {
+        for (int tile = pair_id; tile < g.num_tiles; tile += num_pairs, ++it) {
             int pm, n;
             tile_coords(tile, g, pm, n);
             const int acc = it & 1;
             const uint32_t acc_phase = (it >> 1) & 1;
-            const int row0 = pm * 2 * BM + (int)rank * BM + quarter * 32;
-            const int row = row0 + lane;
-            // 32-column blocks of this warp inside C
-            const int blocks = row0 < g.M ? min(BN / 32, (g.N - n * BN + 31) / 32) : 0;
-            if (has_res && blocks > 0) {
-                if (lane == 0) fetch(n * BN, row0);
-                ++res_issued;
-            }
+            const int row = pm * 2 * BM + (int)rank * BM + quarter * 32 + lane;
+            const int col0 = n * BN + half * (BN / 2);
+            const bool in = row < g.M;
+            const __nv_bfloat16 *res = g.res != nullptr && in ? g.res + row * g.ldr : nullptr;
+            __nv_bfloat16 *y = g.y + row * g.ldy, *z = g.z != nullptr && in ? g.z + row * g.ldz : nullptr;
+            uint32_t q[2][8];
+            if (res != nullptr)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) load16(res + col0 + 16 * h, wide, g.N - col0 - 16 * h, q[h]);
+            const float r = g.epi.inv_rms != nullptr && in ? __ldg(g.epi.inv_rms + row) : 1.f;
             if (!mbar_wait(smem_u32(&acc_full[acc]), acc_phase, &g_linear_error)) break;
             gemm::tc_fence_after();
-            const float r = g.epi.inv_rms != nullptr && row < g.M ? __ldg(g.epi.inv_rms + row) : 1.f;
-            const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * ACC_COLS;
+            const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * ACC_COLS + half * (BN / 2);
 #pragma unroll 1
-            for (int c = 0; c < blocks; ++c, ++blk) {
-                const int col0 = n * BN + c * 32;
-                const uint32_t yb = ybuf + (blk & 1u) * BLOCK_BYTES, zb = zbuf + (blk & 1u) * BLOCK_BYTES;
-                if (has_res) {
-                    if (c + 1 < blocks) {
-                        if (lane == 0) fetch(col0 + 32, row0);
-                        ++res_issued;
-                    }
-                    ok = mbar_wait_fast(rbar + (blk & 1u) * 8u, (blk >> 1) & 1u, &g_linear_error);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    ++res_taken;
-                } else if (lane == 0 && blk >= 2) {
-                    bulk_wait_read1();  // the stores that used these buffers have read them
-                }
-                __syncwarp();
+            for (int c = 0; c < BN / 64; ++c) {
+                const int col = col0 + c * 32;
                 uint32_t v[32];
                 gemm::tmem_ld_32cols(tbase + c * 32, v);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t at = (uint32_t)lane * 64u + (uint32_t)((j ^ ((lane >> 1) & 3)) * 16);
-                    float b[8], f[8];
-                    if (col0 + 8 * j < g.N) load_bias8(g.epi, col0 + 8 * j, b);
-                    else
+                for (int h = 0; h < 2; ++h) {
+                    const int at = col + 16 * h, left = g.N - at;
+                    float f[16];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) b[e] = 0.f;
+                    for (int k = 0; k < 2; ++k) {
+                        float b[8];
+                        if (left > 8 * k) load_bias8(g.epi, at + 8 * k, b);
+                        else
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = fmaf(__uint_as_float(v[8 * j + e]), r, b[e]);
-                    if (has_z) {
-                        const uint4 o = Chunk<__nv_bfloat16>::pack(f);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                                     ::"r"(zb + at), "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w) : "memory");
+                            for (int e = 0; e < 8; ++e) b[e] = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[8 * k + e] = fmaf(__uint_as_float(v[16 * h + 8 * k + e]), r, b[e]);
                     }
+                    if (z != nullptr) store16(z + at, wide, left, f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = activate<ACT>(f[e]);
-                    if (has_res) {
-                        uint4 q;
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(yb + at) : "memory");
-                        float s[8];
-                        Chunk<__nv_bfloat16>::unpack(q, s);
+                    for (int e = 0; e < 16; ++e) f[e] = activate<ACT>(f[e]);
+                    if (res != nullptr) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] += s[e];
+                        for (int e = 0; e < 8; ++e) {
+                            f[2 * e] += bf16lo(q[h][e]);
+                            f[2 * e + 1] += bf16hi(q[h][e]);
+                        }
+                        // the next block's residual (the bytes of y written here are not among them)
+                        if (c + 1 < BN / 64) load16(res + at + 32, wide, left - 32, q[h]);
                     }
-                    const uint4 o = Chunk<__nv_bfloat16>::pack(f);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                                 ::"r"(yb + at), "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w) : "memory");
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (has_z) tma_store_2d(&tmap_z, zb, col0, row0);
-                    tma_store_2d(&tmap_y, yb, col0, row0);
-                    bulk_commit();
+                    if (in) store16(y + at, wide, left, f);
                 }
             }
             gemm::tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty_leader0 + (uint32_t)acc * 8u);
         }
-        // no copy into or out of the staging blocks is in flight at the exit
-        if (lane == 0) {
-            for (; res_taken < res_issued; ++res_taken)
-                mbar_wait(rbar + (res_taken & 1u) * 8u, (res_taken >> 1) & 1u, &g_linear_error);
-            bulk_wait_all();
-        }
-        __syncwarp();
     }
 
     gemm::tc_fence_before();
@@ -337,19 +335,19 @@ template <bool A_MN, bool B_MN, int ACT>
 qkn_status launch(const Matrix &a, const Matrix &b, const Matrix &y, const Matrix *res, const Matrix *z,
                   const Epilogue &epi, int64_t K, cudaStream_t s) {
     const auto kernel = linear_pair_kernel<A_MN, B_MN, ACT>;
-    CUtensorMap ta, tb, ty, tr, tz;
+    CUtensorMap ta, tb;
     if (qkn_status st = make_tmap_pitched(&ta, a.p, a.rows, a.inner, a.pitch, BK, A_MN ? BK : BM, 128)) return st;
     if (qkn_status st = make_tmap_pitched(&tb, b.p, b.rows, b.inner, b.pitch, BK, B_MN ? BK : BN_CTA, 128)) return st;
-    if (qkn_status st = make_tmap_pitched(&ty, y.p, y.rows, y.inner, y.pitch, 32, 32, 64)) return st;
-    tr = tz = ty;
-    if (res != nullptr)
-        if (qkn_status st = make_tmap_pitched(&tr, res->p, res->rows, res->inner, res->pitch, 32, 32, 64)) return st;
-    if (z != nullptr)
-        if (qkn_status st = make_tmap_pitched(&tz, z->p, z->rows, z->inner, z->pitch, 32, 32, 64)) return st;
     Args g;
     g.epi = epi;
-    g.epi.has_res = res != nullptr;
-    g.epi.has_z = z != nullptr;
+    g.y = static_cast<__nv_bfloat16 *>(const_cast<void *>(y.p));
+    g.ldy = y.pitch;
+    g.res = res ? static_cast<const __nv_bfloat16 *>(res->p) : nullptr;
+    g.ldr = res ? res->pitch : 0;
+    g.z = z ? static_cast<__nv_bfloat16 *>(const_cast<void *>(z->p)) : nullptr;
+    g.ldz = z ? z->pitch : 0;
+    g.wide = aligned(g.y, 32) && g.ldy % 16 == 0 && aligned(g.res, 32) && g.ldr % 16 == 0 && aligned(g.z, 32) &&
+             g.ldz % 16 == 0;
     g.M = (int)y.rows;
     g.N = (int)y.inner;
     g.pm_blocks = (int)((y.rows + 2 * BM - 1) / (2 * BM));
@@ -377,7 +375,12 @@ qkn_status launch(const Matrix &a, const Matrix &b, const Matrix &y, const Matri
     }
     cfg.gridDim = dim3(2 * (unsigned)(g.num_tiles < pairs ? g.num_tiles : pairs), 1, 1);
     cfg.stream = s;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, ty, tr, tz, g);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, g);
     if (e != cudaSuccess) return cuda_fail(e, "linear_pair_kernel launch");
     return check_launch("linear_pair_kernel launch");
 }

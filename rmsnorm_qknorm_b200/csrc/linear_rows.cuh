@@ -1,0 +1,303 @@
+// Fused linear layer for few rows: serving a token or a small batch.
+//
+// Included by linear.cu only (one translation unit: its device error word).
+//
+// With few rows the weights are the traffic: the kernel has to keep enough of
+// W in flight on every SM, and the tensor cores have to take W as the operand
+// of 128 rows (a tile of rows of x would be mostly padding).  So the product
+// is formed transposed, D[feature][token] = sum_k W[n][k] x[m][k], with 128
+// features by BT tokens per CTA (BT = 16, 32, 64 or 128, rows behind the last
+// token read as zero), and K is split over the S CTAs of a cluster so that
+// about two CTAs per SM stream W at once, each through a ring of some 100 KiB
+// filled by TMA.  The S partial tiles stay on chip: every CTA leaves its fp32
+// tile in shared memory, and the tokens of the tile are shared out among the
+// CTAs, which add the S partials in rank order over distributed shared memory
+// and run the epilogue.  No workspace, no atomics: the same bits every time.
+//
+// Roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 take
+// the accumulator out of tensor memory; all six add up and store.
+// Every wait is bounded and records a failure in g_linear_error.
+#pragma once
+
+namespace lin {
+namespace rows {
+
+constexpr int BF = 128;                    // features per CTA
+constexpr int BK = 64;
+constexpr int THREADS = 192;
+constexpr int W_BYTES = BF * BK * 2;       // 16 KiB
+constexpr int kMaxCluster = 8;
+constexpr int kMinBlocks = 4;              // k blocks per CTA at least, where K is split
+template <int BT> constexpr int stage_bytes() { return W_BYTES + BT * BK * 2; }
+// two CTAs per SM: at most 113 KiB each
+template <int BT> constexpr int stages() { return (112 * 1024 - 2048) / stage_bytes<BT>(); }
+template <int BT> constexpr int smem_bytes() { return stages<BT>() * stage_bytes<BT>() + 1024 + 256; }
+
+struct Args {
+    Epilogue epi;
+    const __nv_bfloat16 *res;
+    __nv_bfloat16 *y, *z;
+    int64_t ldr, ldy, ldz;
+    int M, N, k_blocks;
+};
+
+template <int BT>
+__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
+    // bf16 A and B, both K-major, fp32 D, M = 128, N = BT
+    constexpr uint32_t desc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BT >> 3) << 17) | ((uint32_t)(BF >> 4) << 24);
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(desc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+template <int BT, int ACT>
+__global__ void __launch_bounds__(THREADS, 2)
+linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x, const Args g) {
+    constexpr int STAGES = stages<BT>(), STAGE_BYTES = stage_bytes<BT>();
+    constexpr int TMEM_COLS = BT < 32 ? 32 : BT;
+    static_assert(BT * BF * 4 <= STAGES * STAGE_BYTES, "the partial tile reuses the ring");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES), *empty = full + STAGES;
+    uint64_t *acc_full = empty + STAGES;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
+    const int n0 = (int)(blockIdx.x / ranks) * BF, t0 = (int)blockIdx.y * BT;
+    const int kb0 = (int)((int64_t)g.k_blocks * rank / ranks), kb1 = (int)((int64_t)g.k_blocks * (rank + 1) / ranks);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(acc_full), 1);
+        mbar_init_fence();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(tmem_slot)), "r"(TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    gemm::tc_fence_before();
+    __syncthreads();
+    gemm::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    // the previous kernel on the stream has finished before any global memory is touched
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, armed = 0, armed_parity = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_fast(smem_u32(&empty[stage]), phase ^ 1u, &g_linear_error)) break;
+                const uint32_t fb = smem_u32(&full[stage]), sa = smem_u32(smem + stage * STAGE_BYTES);
+                mbar_arrive_expect_tx(fb, STAGE_BYTES);
+                tma_load_2d(sa, &tmap_w, kb * BK, n0, fb);
+                tma_load_2d(sa + W_BYTES, &tmap_x, kb * BK, t0, fb);
+                armed |= 1u << stage;
+                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+            // no copy may still be writing when the ring is reused (immediate on the normal path)
+            for (int s = 0; s < STAGES; ++s)
+                if (armed & (1u << s)) mbar_wait(smem_u32(&full[s]), (armed_parity >> s) & 1u, &g_linear_error);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            const uint64_t a0 = gemm::sw128_kmajor_desc(smem_u32(smem));
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_fast(smem_u32(&full[stage]), phase, &g_linear_error)) break;
+                gemm::tc_fence_after();
+                const uint64_t ad = a0 + (uint64_t)((stage * STAGE_BYTES) >> 4), bd = ad + (uint64_t)(W_BYTES >> 4);
+#pragma unroll
+                for (int k = 0; k < BK / gemm::UMMA_K; ++k)
+                    umma<BT>(tmem_base, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), (kb != kb0 || k != 0) ? 1u : 0u);
+                gemm::umma_commit(smem_u32(&empty[stage]));
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+            gemm::umma_commit(smem_u32(acc_full));  // every MMA issued here has completed
+        }
+        __syncwarp();
+    }
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};  // of this thread's four features in the last step
+    if (g.epi.bias != nullptr && n0 + 4 * lane < g.N) {
+        if (g.epi.bias_bf16) load_weights_batched<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(g.epi.bias) + n0 + 4 * lane, bias);
+        else load_weights_batched<float, 4>(static_cast<const float *>(g.epi.bias) + n0 + 4 * lane, bias);
+    }
+    // every thread: the accumulator is complete and no MMA reads the ring any more
+    mbar_wait(smem_u32(acc_full), 0u, &g_linear_error);
+    gemm::tc_fence_after();
+    __syncthreads();
+    float *tile = reinterpret_cast<float *>(smem);  // [BT tokens][BF features]
+    if (warp >= 2) {
+        const int quarter = warp & 3;
+#pragma unroll 1
+        for (int c = 0; c < BT / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld_16cols(tmem_base + ((uint32_t)(quarter * 32) << 16) + c * 16, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) tile[(c * 16 + i) * BF + quarter * 32 + lane] = __uint_as_float(v[i]);
+        }
+        gemm::tc_fence_before();
+    }
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
+    // Tokens rank, rank + ranks, ... of the tile, a warp per token and four features per thread:
+    // two tokens' partials are asked for before the first is added up.
+    const int valid = min(BT, g.M - t0);
+    const int n = n0 + 4 * lane;
+    constexpr int kStep = THREADS / 32;
+    if (n < g.N) {  // N is a multiple of 8
+        for (int i = warp; rank + i * ranks < valid; i += 2 * kStep) {
+            float4 part[2][kMaxCluster];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int t = min(rank + (i + u * kStep) * ranks, BT - 1);
+                const uint32_t at = smem_u32(tile + t * BF + 4 * lane);
+#pragma unroll
+                for (int s = 0; s < kMaxCluster; ++s)
+                    if (s < ranks) part[u][s] = ld_cluster_f32x4(map_to_rank(at, (uint32_t)s));
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int t = rank + (i + u * kStep) * ranks;
+                if (t >= valid) break;
+                float v[4] = {part[u][0].x, part[u][0].y, part[u][0].z, part[u][0].w};
+#pragma unroll
+                for (int s = 1; s < kMaxCluster; ++s)
+                    if (s < ranks) {
+                        v[0] += part[u][s].x;
+                        v[1] += part[u][s].y;
+                        v[2] += part[u][s].z;
+                        v[3] += part[u][s].w;
+                    }
+                const int64_t m = t0 + t;
+                const float r = g.epi.inv_rms != nullptr ? __ldg(g.epi.inv_rms + m) : 1.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = fmaf(v[e], r, bias[e]);
+                if (g.z != nullptr)
+                    *reinterpret_cast<uint2 *>(g.z + m * g.ldz + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = activate<ACT>(v[e]);
+                if (g.res != nullptr) {
+                    const uint2 q = *reinterpret_cast<const uint2 *>(g.res + m * g.ldr + n);  // may be y itself
+                    v[0] += bf16lo(q.x);
+                    v[1] += bf16hi(q.x);
+                    v[2] += bf16lo(q.y);
+                    v[3] += bf16hi(q.y);
+                }
+                *reinterpret_cast<uint2 *>(g.y + m * g.ldy + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            }
+        }
+    }
+    if (ranks > 1) cluster_sync();  // the other CTAs have read this one's tile
+    else __syncthreads();
+    if (warp == 1) {
+        gemm::tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+template <int BT, int ACT>
+qkn_status launch_bt(const pair::Matrix &x, const pair::Matrix &W, const Args &a, cudaStream_t s) {
+    const auto kernel = linear_rows_kernel<BT, ACT>;
+    CUtensorMap tw, tx;
+    if (qkn_status st = make_tmap_pitched(&tw, W.p, W.rows, W.inner, W.pitch, BK, BF, 128)) return st;
+    if (qkn_status st = make_tmap_pitched(&tx, x.p, x.rows, x.inner, x.pitch, BK, BT, 128)) return st;
+    static std::atomic<bool> attr_set[64];  // per device: the attribute has been set
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const bool known = dev >= 0 && dev < 64;
+    if (!known || !attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<BT>());
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear_rows_kernel)");
+        if (known) attr_set[dev].store(true, std::memory_order_release);
+    }
+    const int64_t tiles = (a.N + BF - 1) / BF, token_tiles = (a.M + BT - 1) / BT;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem_bytes<BT>();
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    // K is split over as many CTAs as leave every cluster resident at once (a second wave costs
+    // more than the wider split gains: one token, 12288 x 4096, 21.6 us over 192 CTAs, 29.9 us
+    // over 288 that do not all fit), each over at least kMinBlocks blocks of k
+    static std::atomic<int> resident[64][kMaxCluster + 1];  // per device and cluster size; 0 until asked
+    int64_t split = kMaxCluster;
+    if (split > a.k_blocks / kMinBlocks) split = a.k_blocks / kMinBlocks;
+    for (; split > 1; --split) {
+        int n = known ? resident[dev][split].load(std::memory_order_relaxed) : 0;
+        if (n == 0) {
+            attr[0].val.clusterDim.x = (unsigned)split;
+            cfg.gridDim = dim3((unsigned)split, 1, 1);
+            cfg.numAttrs = 1;
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(linear_rows_kernel)");
+            if (n < 1) n = 1;
+            if (known) resident[dev][split].store(n, std::memory_order_relaxed);
+        }
+        if (tiles * token_tiles <= n) break;
+    }
+    if (split < 1) split = 1;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)token_tiles, 1);
+    attr[0].val.clusterDim.x = (unsigned)split;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tw, tx, a);
+    if (e != cudaSuccess) return cuda_fail(e, "linear_rows_kernel launch");
+    return check_launch("linear_rows_kernel launch");
+}
+
+template <int ACT>
+qkn_status launch(const pair::Matrix &x, const pair::Matrix &W, const pair::Matrix &y, const pair::Matrix *res,
+                  const pair::Matrix *z, const Epilogue &epi, int64_t K, cudaStream_t s) {
+    Args a;
+    a.epi = epi;
+    a.res = res ? static_cast<const __nv_bfloat16 *>(res->p) : nullptr;
+    a.z = z ? static_cast<__nv_bfloat16 *>(const_cast<void *>(z->p)) : nullptr;
+    a.y = static_cast<__nv_bfloat16 *>(const_cast<void *>(y.p));
+    a.ldr = res ? res->pitch : 0;
+    a.ldz = z ? z->pitch : 0;
+    a.ldy = y.pitch;
+    a.M = (int)y.rows;
+    a.N = (int)y.inner;
+    a.k_blocks = (int)((K + BK - 1) / BK);
+    if (a.M <= 16) return launch_bt<16, ACT>(x, W, a, s);
+    if (a.M <= 32) return launch_bt<32, ACT>(x, W, a, s);
+    if (a.M <= 64) return launch_bt<64, ACT>(x, W, a, s);
+    return launch_bt<128, ACT>(x, W, a, s);
+}
+
+}  // namespace rows
+}  // namespace lin
