@@ -2,7 +2,7 @@
 //
 // Included by linear.cu only (one translation unit: its device error word).
 //
-//   C[m][n] = sum_k A(m, k) B(n, k),  256 x 256 tiles of C, bf16 in, fp32
+//   C[m][n] = sum_k A(m, k) B(n, k),  256 x 256 (or 128) tiles of C, bf16 in, fp32
 // accumulated in tensor memory by tcgen05.mma.cta_group::2.  An operand is
 // K-major (rows of consecutive k: x and W of the forward product) or MN-major
 // (consecutive m or n: W in dx = dz W, dz and x in dW = dz^T x), read where it
@@ -26,18 +26,24 @@
 namespace lin {
 namespace pair {
 
-constexpr int BM = 128, BN = 256, BN_CTA = 128, BK = 64;
-constexpr int STAGES = 7;
-constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN_CTA * BK * 2;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int PAIR_STAGE_BYTES = 2 * STAGE_BYTES;
-constexpr int ACC_COLS = BN, TMEM_COLS = 2 * ACC_COLS;
+constexpr int BM = 128, BK = 64;                   // rows per CTA (256 per pair), k per stage
+constexpr int A_BYTES = BM * BK * 2;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int BAR_BYTES = 256;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BAR_BYTES + 1024;
+
+// The tile's columns: 256, or 128 where the wider tiles leave pairs without work.
+template <int BN> struct Shape {
+    static constexpr int BN_CTA = BN / 2;          // rows of B that each CTA loads
+    static constexpr int B_BYTES = BN_CTA * BK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = (226 * 1024 - BAR_BYTES - 1024) / STAGE_BYTES;
+    static constexpr int PAIR_STAGE_BYTES = 2 * STAGE_BYTES;
+    static constexpr int TMEM_COLS = 2 * BN;       // two accumulators
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BAR_BYTES + 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024 && (2 * STAGES + 6) * 8 <= BAR_BYTES, "shared memory budget");
+};
 constexpr int GROUP_M = 16;  // pair row blocks walked together down each column block (operands shared in L2)
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
 struct Args {
     Epilogue epi;
@@ -59,9 +65,9 @@ __device__ __forceinline__ void tile_coords(int tile, const Args &g, int &pm, in
     n = in_group / rows_in_group;
 }
 
-// Instruction descriptor: bf16 A and B, fp32 D, M = 256 (the pair), N = 256;
+// Instruction descriptor: bf16 A and B, fp32 D, M = 256 (the pair), N = BN;
 // bits 15 and 16 mark MN-major operands.
-template <bool A_MN, bool B_MN> constexpr uint32_t instr_desc() {
+template <bool A_MN, bool B_MN, int BN> constexpr uint32_t instr_desc() {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
            ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(2 * BM >> 4) << 24);
 }
@@ -91,12 +97,12 @@ __device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t adesc, uint64_t b
                  ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate));
 }
 
-// One operand's 128 rows x 64 k into a stage of this CTA.
-template <bool MN>
+// ROWS rows x 64 k of an operand into a stage of this CTA.
+template <bool MN, int ROWS>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int row, int k, uint32_t bar) {
     if constexpr (MN) {
-        qkn::pair::tma_load_2d_pair(dst, map, row, k, bar);
-        qkn::pair::tma_load_2d_pair(dst + 8192u, map, row + 64, k, bar);
+#pragma unroll
+        for (int h = 0; h < ROWS / 64; ++h) qkn::pair::tma_load_2d_pair(dst + h * 8192u, map, row + 64 * h, k, bar);
     } else {
         qkn::pair::tma_load_2d_pair(dst, map, k, row, bar);
     }
@@ -136,10 +142,12 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *p, bool wide, int left, c
         if (left > 8 * h) *reinterpret_cast<uint4 *>(p + 8 * h) = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
 }
 
-template <bool A_MN, bool B_MN, int ACT>
+template <bool A_MN, bool B_MN, int BN, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                    const Args g) {
+    using S = Shape<BN>;
+    constexpr int STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, BN_CTA = S::BN_CTA;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES);
@@ -167,7 +175,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     }
     if (warp == 1) {  // whole warp, in both CTAs: the pair's tensor memory
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(smem_u32(tmem_slot)), "r"(TMEM_COLS) : "memory");
+                     ::"r"(smem_u32(tmem_slot)), "r"(S::TMEM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     gemm::tc_fence_before();
@@ -191,11 +199,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
                 tile_coords(tile, g, pm, n);
                 for (int kb = 0; kb < g.k_blocks; ++kb) {
                     if (!mbar_wait_fast(smem_u32(&empty[stage]), phase ^ 1u, &g_linear_error)) { ok = false; break; }
-                    if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), PAIR_STAGE_BYTES);
+                    if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), S::PAIR_STAGE_BYTES);
                     const uint32_t fb = fb0 + (uint32_t)stage * 8u;
                     const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
-                    load_operand<A_MN>(sa, &tmap_a, pm * 2 * BM + (int)rank * BM, kb * BK, fb);
-                    load_operand<B_MN>(sa + A_BYTES, &tmap_b, n * BN + (int)rank * BN_CTA, kb * BK, fb);
+                    load_operand<A_MN, BM>(sa, &tmap_a, pm * 2 * BM + (int)rank * BM, kb * BK, fb);
+                    load_operand<B_MN, BN_CTA>(sa + A_BYTES, &tmap_b, n * BN + (int)rank * BN_CTA, kb * BK, fb);
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -225,14 +233,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
                 const uint32_t acc_phase = (it >> 1) & 1;
                 if (!mbar_wait_cluster(smem_u32(&acc_empty[acc]), acc_phase ^ 1u, &g_linear_error)) break;
                 gemm::tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
+                const uint32_t d_tmem = tmem_base + acc * BN;
                 for (int kb = 0; kb < g.k_blocks; ++kb) {
                     if (!mbar_wait_fast(smem_u32(&full[stage]), phase, &g_linear_error)) { ok = false; break; }
                     gemm::tc_fence_after();
                     const uint64_t at = (uint64_t)((stage * STAGE_BYTES) >> 4);
 #pragma unroll
                     for (int k = 0; k < BK / gemm::UMMA_K; ++k)
-                        umma<instr_desc<A_MN, B_MN>()>(d_tmem, a_desc0 + at + k * k_step<A_MN>(),
+                        umma<instr_desc<A_MN, B_MN, BN>()>(d_tmem, a_desc0 + at + k * k_step<A_MN>(),
                                                        b_desc0 + at + k * k_step<B_MN>(), (kb | k) != 0 ? 1u : 0u);
                     // the stage is free in both CTAs once these MMAs have read it
                     qkn::pair::umma_commit_pair(smem_u32(&empty[stage]));
@@ -272,7 +280,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             const float r = g.epi.inv_rms != nullptr && in ? __ldg(g.epi.inv_rms + row) : 1.f;
             if (!mbar_wait(smem_u32(&acc_full[acc]), acc_phase, &g_linear_error)) break;
             gemm::tc_fence_after();
-            const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * ACC_COLS + half * (BN / 2);
+            const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN + half * (BN / 2);
 #pragma unroll 1
             for (int c = 0; c < BN / 64; ++c) {
                 const int col = col0 + c * 32;
@@ -318,7 +326,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     cluster_sync();  // the even CTA's MMAs and copies, which use both CTAs' memory, are done
     if (warp == 1) {
         gemm::tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(S::TMEM_COLS)
                      : "memory");
     }
 }
@@ -331,27 +339,15 @@ struct Matrix {
     int64_t rows, inner, pitch;
 };
 
-template <bool A_MN, bool B_MN, int ACT>
-qkn_status launch(const Matrix &a, const Matrix &b, const Matrix &y, const Matrix *res, const Matrix *z,
-                  const Epilogue &epi, int64_t K, cudaStream_t s) {
-    const auto kernel = linear_pair_kernel<A_MN, B_MN, ACT>;
+template <bool A_MN, bool B_MN, int BN, int ACT>
+qkn_status launch_bn(const Matrix &a, const Matrix &b, Args &g, int64_t K, cudaStream_t s) {
+    using S = Shape<BN>;
+    const auto kernel = linear_pair_kernel<A_MN, B_MN, BN, ACT>;
     CUtensorMap ta, tb;
     if (qkn_status st = make_tmap_pitched(&ta, a.p, a.rows, a.inner, a.pitch, BK, A_MN ? BK : BM, 128)) return st;
-    if (qkn_status st = make_tmap_pitched(&tb, b.p, b.rows, b.inner, b.pitch, BK, B_MN ? BK : BN_CTA, 128)) return st;
-    Args g;
-    g.epi = epi;
-    g.y = static_cast<__nv_bfloat16 *>(const_cast<void *>(y.p));
-    g.ldy = y.pitch;
-    g.res = res ? static_cast<const __nv_bfloat16 *>(res->p) : nullptr;
-    g.ldr = res ? res->pitch : 0;
-    g.z = z ? static_cast<__nv_bfloat16 *>(const_cast<void *>(z->p)) : nullptr;
-    g.ldz = z ? z->pitch : 0;
-    g.wide = aligned(g.y, 32) && g.ldy % 16 == 0 && aligned(g.res, 32) && g.ldr % 16 == 0 && aligned(g.z, 32) &&
-             g.ldz % 16 == 0;
-    g.M = (int)y.rows;
-    g.N = (int)y.inner;
-    g.pm_blocks = (int)((y.rows + 2 * BM - 1) / (2 * BM));
-    g.n_blocks = (int)((y.inner + BN - 1) / BN);
+    if (qkn_status st = make_tmap_pitched(&tb, b.p, b.rows, b.inner, b.pitch, BK, B_MN ? BK : S::BN_CTA, 128)) return st;
+    g.pm_blocks = (int)(((int64_t)g.M + 2 * BM - 1) / (2 * BM));
+    g.n_blocks = (int)(((int64_t)g.N + BN - 1) / BN);
     g.k_blocks = (int)((K + BK - 1) / BK);
     if ((int64_t)g.pm_blocks * g.n_blocks > 0x7fffffffLL) return fail(QKN_ERR_SHAPE, "linear_pair_kernel: too many tiles");
     g.num_tiles = g.pm_blocks * g.n_blocks;
@@ -362,9 +358,9 @@ qkn_status launch(const Matrix &a, const Matrix &b, const Matrix &y, const Matri
     int pairs = known ? max_pairs[dev].load(std::memory_order_acquire) : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.dynamicSmemBytes = S::SMEM_BYTES;
     if (pairs == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear_pair_kernel)");
         cfg.gridDim = dim3(2 * (unsigned)(sm_count() / 2), 1, 1);
         int n = 0;
@@ -383,6 +379,28 @@ qkn_status launch(const Matrix &a, const Matrix &b, const Matrix &y, const Matri
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, g);
     if (e != cudaSuccess) return cuda_fail(e, "linear_pair_kernel launch");
     return check_launch("linear_pair_kernel launch");
+}
+
+template <bool A_MN, bool B_MN, int ACT>
+qkn_status launch(const Matrix &a, const Matrix &b, const Matrix &y, const Matrix *res, const Matrix *z,
+                  const Epilogue &epi, int64_t K, cudaStream_t s) {
+    Args g;
+    g.epi = epi;
+    g.y = static_cast<__nv_bfloat16 *>(const_cast<void *>(y.p));
+    g.ldy = y.pitch;
+    g.res = res ? static_cast<const __nv_bfloat16 *>(res->p) : nullptr;
+    g.ldr = res ? res->pitch : 0;
+    g.z = z ? static_cast<__nv_bfloat16 *>(const_cast<void *>(z->p)) : nullptr;
+    g.ldz = z ? z->pitch : 0;
+    g.wide = aligned(g.y, 32) && g.ldy % 16 == 0 && aligned(g.res, 32) && g.ldr % 16 == 0 && aligned(g.z, 32) &&
+             g.ldz % 16 == 0;
+    g.M = (int)y.rows;
+    g.N = (int)y.inner;
+    const int64_t pm = (y.rows + 2 * BM - 1) / (2 * BM), pairs = sm_count() / 2;
+    const int64_t w256 = (pm * ((y.inner + 255) / 256) + pairs - 1) / pairs, w128 = (pm * ((y.inner + 127) / 128) + pairs - 1) / pairs;
+    bool narrow = 8 * w128 < 13 * w256;
+    if (const char *v = getenv("LIN_BN")) narrow = atoi(v) == 128;
+    return narrow ? launch_bn<A_MN, B_MN, 128, ACT>(a, b, g, K, s) : launch_bn<A_MN, B_MN, 256, ACT>(a, b, g, K, s);
 }
 
 }  // namespace pair

@@ -66,6 +66,60 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     return v;
 }
 
+// Adds up the partials of this CTA's tokens and runs the epilogue: a warp per
+// token, four features per thread, TOKENS tokens at a time.
+template <int ACT, int MAX_RANKS, int TOKENS, int BT>
+__device__ __forceinline__ void finish(const Args &g, uint32_t tile, const float (&bias)[4], int n0, int t0, int rank,
+                                       int ranks) {
+    constexpr int kStep = THREADS / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int valid = min(BT, g.M - t0), n = n0 + 4 * lane;
+    if (n >= g.N) return;  // N is a multiple of 8
+    for (int i = warp; rank + i * ranks < valid; i += TOKENS * kStep) {
+        float4 part[TOKENS][MAX_RANKS];
+        uint2 q[TOKENS];
+#pragma unroll
+        for (int u = 0; u < TOKENS; ++u) {
+            const int t = rank + (i + u * kStep) * ranks;
+            q[u] = make_uint2(0u, 0u);
+            if (t >= valid) continue;
+#pragma unroll
+            for (int s = 0; s < MAX_RANKS; ++s)
+                if (s < ranks) part[u][s] = ld_cluster_f32x4(map_to_rank(tile + (uint32_t)(t * BF + 4 * lane) * 4u, (uint32_t)s));
+            if (g.res != nullptr) q[u] = *reinterpret_cast<const uint2 *>(g.res + (int64_t)(t0 + t) * g.ldr + n);  // may be y itself
+        }
+#pragma unroll
+        for (int u = 0; u < TOKENS; ++u) {
+            const int t = rank + (i + u * kStep) * ranks;
+            if (t >= valid) continue;
+            float v[4] = {part[u][0].x, part[u][0].y, part[u][0].z, part[u][0].w};
+#pragma unroll
+            for (int s = 1; s < MAX_RANKS; ++s)
+                if (s < ranks) {
+                    v[0] += part[u][s].x;
+                    v[1] += part[u][s].y;
+                    v[2] += part[u][s].z;
+                    v[3] += part[u][s].w;
+                }
+            const int64_t m = t0 + t;
+            const float r = g.epi.inv_rms != nullptr ? __ldg(g.epi.inv_rms + m) : 1.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(v[e], r, bias[e]);
+            if (g.z != nullptr)
+                *reinterpret_cast<uint2 *>(g.z + m * g.ldz + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = activate<ACT>(v[e]);
+            if (g.res != nullptr) {
+                v[0] += bf16lo(q[u].x);
+                v[1] += bf16hi(q[u].x);
+                v[2] += bf16lo(q[u].y);
+                v[3] += bf16hi(q[u].y);
+            }
+            *reinterpret_cast<uint2 *>(g.y + m * g.ldy + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        }
+    }
+}
+
 template <int BT, int ACT>
 __global__ void __launch_bounds__(THREADS, 2)
 linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x, const Args g) {
@@ -166,54 +220,12 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
     }
     if (ranks > 1) cluster_sync();
     else __syncthreads();
-    // Tokens rank, rank + ranks, ... of the tile, a warp per token and four features per thread:
-    // two tokens' partials are asked for before the first is added up.
-    const int valid = min(BT, g.M - t0);
-    const int n = n0 + 4 * lane;
-    constexpr int kStep = THREADS / 32;
-    if (n < g.N) {  // N is a multiple of 8
-        for (int i = warp; rank + i * ranks < valid; i += 2 * kStep) {
-            float4 part[2][kMaxCluster];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = min(rank + (i + u * kStep) * ranks, BT - 1);
-                const uint32_t at = smem_u32(tile + t * BF + 4 * lane);
-#pragma unroll
-                for (int s = 0; s < kMaxCluster; ++s)
-                    if (s < ranks) part[u][s] = ld_cluster_f32x4(map_to_rank(at, (uint32_t)s));
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = rank + (i + u * kStep) * ranks;
-                if (t >= valid) break;
-                float v[4] = {part[u][0].x, part[u][0].y, part[u][0].z, part[u][0].w};
-#pragma unroll
-                for (int s = 1; s < kMaxCluster; ++s)
-                    if (s < ranks) {
-                        v[0] += part[u][s].x;
-                        v[1] += part[u][s].y;
-                        v[2] += part[u][s].z;
-                        v[3] += part[u][s].w;
-                    }
-                const int64_t m = t0 + t;
-                const float r = g.epi.inv_rms != nullptr ? __ldg(g.epi.inv_rms + m) : 1.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = fmaf(v[e], r, bias[e]);
-                if (g.z != nullptr)
-                    *reinterpret_cast<uint2 *>(g.z + m * g.ldz + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = activate<ACT>(v[e]);
-                if (g.res != nullptr) {
-                    const uint2 q = *reinterpret_cast<const uint2 *>(g.res + m * g.ldr + n);  // may be y itself
-                    v[0] += bf16lo(q.x);
-                    v[1] += bf16hi(q.x);
-                    v[2] += bf16lo(q.y);
-                    v[3] += bf16hi(q.y);
-                }
-                *reinterpret_cast<uint2 *>(g.y + m * g.ldy + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-            }
-        }
-    }
+    // Tokens rank, rank + ranks, ... of the tile: up to 16 partials of a thread's four features
+    // are asked for before the first is added
+    const uint32_t at = smem_u32(tile);
+    if (ranks <= 2) finish<ACT, 2, 8, BT>(g, at, bias, n0, t0, rank, ranks);
+    else if (ranks <= 4) finish<ACT, 4, 4, BT>(g, at, bias, n0, t0, rank, ranks);
+    else finish<ACT, kMaxCluster, 2, BT>(g, at, bias, n0, t0, rank, ranks);
     if (ranks > 1) cluster_sync();  // the other CTAs have read this one's tile
     else __syncthreads();
     if (warp == 1) {
