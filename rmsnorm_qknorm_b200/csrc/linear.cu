@@ -15,6 +15,7 @@
 #include "pair_tc.cuh"
 #include "qkn_common.cuh"
 #include "qkn_sync.cuh"
+#include "linear_issue.cuh"
 
 namespace qkn {
 

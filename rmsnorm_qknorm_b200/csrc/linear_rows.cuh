@@ -41,13 +41,9 @@ struct Args {
     int M, N, k_blocks;
 };
 
-template <int BT>
-__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
-    // bf16 A and B, both K-major, fp32 D, M = 128, N = BT
-    constexpr uint32_t desc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BT >> 3) << 17) | ((uint32_t)(BF >> 4) << 24);
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(desc), "r"(accumulate));
+// bf16 A and B, both K-major, fp32 D, M = 128, N = BT
+template <int BT> constexpr uint32_t instr_desc() {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BT >> 3) << 17) | ((uint32_t)(BF >> 4) << 24);
 }
 
 __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
@@ -159,42 +155,39 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, armed = 0, armed_parity = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait_fast(smem_u32(&empty[stage]), phase ^ 1u, &g_linear_error)) break;
-                const uint32_t fb = smem_u32(&full[stage]), sa = smem_u32(smem + stage * STAGE_BYTES);
-                mbar_arrive_expect_tx(fb, STAGE_BYTES);
-                tma_load_2d(sa, &tmap_w, kb * BK, n0, fb);
-                tma_load_2d(sa + W_BYTES, &tmap_x, kb * BK, t0, fb);
-                armed |= 1u << stage;
-                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-            }
-            // no copy may still be writing when the ring is reused (immediate on the normal path)
-            for (int s = 0; s < STAGES; ++s)
-                if (armed & (1u << s)) mbar_wait(smem_u32(&full[s]), (armed_parity >> s) & 1u, &g_linear_error);
+        int stage = 0;
+        uint32_t phase = 0, armed = 0, armed_parity = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, &g_linear_error)) break;
+            const uint32_t fb = smem_u32(&full[stage]), sa = smem_u32(smem + stage * STAGE_BYTES);
+            elect_expect_tx(fb, STAGE_BYTES);
+            elect_tma_load(sa, &tmap_w, kb * BK, n0, fb);
+            elect_tma_load(sa + W_BYTES, &tmap_x, kb * BK, t0, fb);
+            armed |= 1u << stage;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
+        // no copy may still be writing when the ring is reused (immediate on the normal path)
+        for (int s = 0; s < STAGES; ++s)
+            if (armed & (1u << s)) mbar_wait(smem_u32(&full[s]), (armed_parity >> s) & 1u, &g_linear_error);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            const uint64_t a0 = gemm::sw128_kmajor_desc(smem_u32(smem));
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait_fast(smem_u32(&full[stage]), phase, &g_linear_error)) break;
-                gemm::tc_fence_after();
-                const uint64_t ad = a0 + (uint64_t)((stage * STAGE_BYTES) >> 4), bd = ad + (uint64_t)(W_BYTES >> 4);
+        const uint64_t a0 = gemm::sw128_kmajor_desc(smem_u32(smem));
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!warp_wait(smem_u32(&full[stage]), phase, &g_linear_error)) break;
+            gemm::tc_fence_after();
+            const uint64_t ad = a0 + (uint64_t)((stage * STAGE_BYTES) >> 4), bd = ad + (uint64_t)(W_BYTES >> 4);
 #pragma unroll
-                for (int k = 0; k < BK / gemm::UMMA_K; ++k)
-                    umma<BT>(tmem_base, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), (kb != kb0 || k != 0) ? 1u : 0u);
-                gemm::umma_commit(smem_u32(&empty[stage]));
-                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-            }
-            gemm::umma_commit(smem_u32(acc_full));  // every MMA issued here has completed
+            for (int k = 0; k < BK / gemm::UMMA_K; ++k)
+                elect_umma<1, instr_desc<BT>()>(tmem_base, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k),
+                                                (kb != kb0 || k != 0) ? 1u : 0u);
+            elect_commit<1>(smem_u32(&empty[stage]));
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
+        elect_commit<1>(smem_u32(acc_full));  // every MMA issued here has completed
         __syncwarp();
     }
     float bias[4] = {0.f, 0.f, 0.f, 0.f};  // of this thread's four features in the last step
