@@ -90,21 +90,14 @@ template <bool MN> __device__ __forceinline__ uint64_t operand_desc(uint32_t sad
 // 16 k further: 32 bytes along a K-major row, two groups of 8 k MN-major.
 template <bool MN> constexpr uint64_t k_step() { return MN ? 2048u >> 4 : 32u >> 4; }
 
-template <uint32_t IDESC>
-__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate));
-}
-
 // ROWS rows x 64 k of an operand into a stage of this CTA.
 template <bool MN, int ROWS>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int row, int k, uint32_t bar) {
     if constexpr (MN) {
 #pragma unroll
-        for (int h = 0; h < ROWS / 64; ++h) qkn::pair::tma_load_2d_pair(dst + h * 8192u, map, row + 64 * h, k, bar);
+        for (int h = 0; h < ROWS / 64; ++h) elect_tma_load_pair(dst + h * 8192u, map, row + 64 * h, k, bar);
     } else {
-        qkn::pair::tma_load_2d_pair(dst, map, k, row, bar);
+        elect_tma_load_pair(dst, map, k, row, bar);
     }
 }
 
@@ -188,38 +181,36 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer (both CTAs)
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            uint32_t armed = 0, armed_parity = 0;  // per stage: loads issued; parity of the phase they complete
-            bool ok = true;
-            const uint32_t fb0 = map_to_rank(smem_u32(&full[0]), 0);  // the even CTA's stage barriers
-            for (int tile = pair_id; ok && tile < g.num_tiles; tile += num_pairs) {
-                int pm, n;
-                tile_coords(tile, g, pm, n);
-                for (int kb = 0; kb < g.k_blocks; ++kb) {
-                    if (!mbar_wait_fast(smem_u32(&empty[stage]), phase ^ 1u, &g_linear_error)) { ok = false; break; }
-                    if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), S::PAIR_STAGE_BYTES);
-                    const uint32_t fb = fb0 + (uint32_t)stage * 8u;
-                    const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
-                    load_operand<A_MN, BM>(sa, &tmap_a, pm * 2 * BM + (int)rank * BM, kb * BK, fb);
-                    load_operand<B_MN, BN_CTA>(sa + A_BYTES, &tmap_b, n * BN + (int)rank * BN_CTA, kb * BK, fb);
-                    armed |= 1u << stage;
-                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                }
+        int stage = 0;
+        uint32_t phase = 0;
+        uint32_t armed = 0, armed_parity = 0;  // per stage: loads issued; parity of the phase they complete
+        bool ok = true;
+        const uint32_t fb0 = map_to_rank(smem_u32(&full[0]), 0);  // the even CTA's stage barriers
+        for (int tile = pair_id; ok && tile < g.num_tiles; tile += num_pairs) {
+            int pm, n;
+            tile_coords(tile, g, pm, n);
+            const int row = pm * 2 * BM + (int)rank * BM, col = n * BN + (int)rank * BN_CTA;
+            for (int kb = 0; kb < g.k_blocks; ++kb) {
+                if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, &g_linear_error)) { ok = false; break; }
+                if (leader) elect_expect_tx(smem_u32(&full[stage]), S::PAIR_STAGE_BYTES);
+                const uint32_t fb = fb0 + (uint32_t)stage * 8u;
+                const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
+                load_operand<A_MN, BM>(sa, &tmap_a, row, kb * BK, fb);
+                load_operand<B_MN, BN_CTA>(sa + A_BYTES, &tmap_b, col, kb * BK, fb);
+                armed |= 1u << stage;
+                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
-            // no copy of either CTA is in flight when the pair exits (the odd CTA stays until the
-            // cluster barrier below; immediate on the normal path)
-            if (leader)
-                for (int s2 = 0; s2 < STAGES; ++s2)
-                    if (armed & (1u << s2))
-                        mbar_wait(smem_u32(&full[s2]), (armed_parity >> s2) & 1u, &g_linear_error);
         }
+        // no copy of either CTA is in flight when the pair exits (the odd CTA stays until the
+        // cluster barrier below; immediate on the normal path)
+        if (leader)
+            for (int s2 = 0; s2 < STAGES; ++s2)
+                if (armed & (1u << s2)) mbar_wait(smem_u32(&full[s2]), (armed_parity >> s2) & 1u, &g_linear_error);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer (even CTA)
-        if (leader && lane == 0) {
+        if (leader) {
             const uint32_t peer_empty0 = map_to_rank(smem_u32(&empty[0]), 1);
             const uint32_t peer_acc_full0 = map_to_rank(smem_u32(&acc_full[0]), 1);
             const uint64_t a_desc0 = operand_desc<A_MN>(smem_u32(smem));
@@ -231,28 +222,28 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             for (int tile = pair_id; ok && tile < g.num_tiles; tile += num_pairs, ++it) {
                 const int acc = it & 1;
                 const uint32_t acc_phase = (it >> 1) & 1;
-                if (!mbar_wait_cluster(smem_u32(&acc_empty[acc]), acc_phase ^ 1u, &g_linear_error)) break;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&acc_empty[acc]), acc_phase ^ 1u, &g_linear_error))) break;
                 gemm::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * BN;
                 for (int kb = 0; kb < g.k_blocks; ++kb) {
-                    if (!mbar_wait_fast(smem_u32(&full[stage]), phase, &g_linear_error)) { ok = false; break; }
+                    if (!warp_wait(smem_u32(&full[stage]), phase, &g_linear_error)) { ok = false; break; }
                     gemm::tc_fence_after();
                     const uint64_t at = (uint64_t)((stage * STAGE_BYTES) >> 4);
 #pragma unroll
                     for (int k = 0; k < BK / gemm::UMMA_K; ++k)
-                        umma<instr_desc<A_MN, B_MN, BN>()>(d_tmem, a_desc0 + at + k * k_step<A_MN>(),
-                                                       b_desc0 + at + k * k_step<B_MN>(), (kb | k) != 0 ? 1u : 0u);
+                        elect_umma<2, instr_desc<A_MN, B_MN, BN>()>(d_tmem, a_desc0 + at + k * k_step<A_MN>(),
+                                                                    b_desc0 + at + k * k_step<B_MN>(), (kb | k) != 0 ? 1u : 0u);
                     // the stage is free in both CTAs once these MMAs have read it
-                    qkn::pair::umma_commit_pair(smem_u32(&empty[stage]));
-                    qkn::pair::umma_commit_pair(peer_empty0 + (uint32_t)stage * 8u);
+                    elect_commit<2>(smem_u32(&empty[stage]));
+                    elect_commit<2>(peer_empty0 + (uint32_t)stage * 8u);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
-                qkn::pair::umma_commit_pair(smem_u32(&acc_full[acc]));
-                qkn::pair::umma_commit_pair(peer_acc_full0 + (uint32_t)acc * 8u);
+                elect_commit<2>(smem_u32(&acc_full[acc]));
+                elect_commit<2>(peer_acc_full0 + (uint32_t)acc * 8u);
             }
             // tensor memory is released only after every MMA issued here has completed
-            qkn::pair::umma_commit_pair(smem_u32(drained));
+            elect_commit<2>(smem_u32(drained));
             mbar_wait(smem_u32(drained), 0u, &g_linear_error);
         }
         __syncwarp();
