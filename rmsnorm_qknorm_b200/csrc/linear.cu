@@ -5,17 +5,17 @@
 // The products run on the tensor cores (linear_pair.cuh) with everything else
 // in their epilogue; dz is formed once (and rounded to bf16, the products'
 // operand type) by an element-wise pass that adds up db in fp32 on the way.
+#include <algorithm>
 #include <atomic>
 #include <cuda.h>
 #include <math.h>
-#include <stdlib.h>
 
 #include "gemm_tc.cuh"
+#include "linear_issue.cuh"
 #include "linear_math.cuh"
 #include "pair_tc.cuh"
 #include "qkn_common.cuh"
 #include "qkn_sync.cuh"
-#include "linear_issue.cuh"
 
 namespace qkn {
 
@@ -30,44 +30,66 @@ namespace lin {
 // ---------------------------------------------------------------- dz and db
 
 // dz = dy act'(z) and the partial column sums of dz: a block walks the rows of
-// its slice over 256 columns, 8 rows at a time, a 16-byte chunk per thread;
-// the eight rows' sums meet in shared memory in row order.
-constexpr int kDzCols = 256, kDzThreads = 256;
+// its slice over 256 columns, a 16-byte chunk per thread, eight rows side by
+// side and four of those groups at a time, all their loads issued before any
+// arithmetic; the eight rows' sums meet in shared memory in row order.
+constexpr int kDzCols = 256, kDzThreads = 256, kDzRows = 8, kDzUnroll = 4;
 
+template <int ACT>
 __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const __nv_bfloat16 *__restrict__ dy,
                                                                const __nv_bfloat16 *__restrict__ z,
                                                                __nv_bfloat16 *__restrict__ dz, float *__restrict__ part,
-                                                               int64_t M, int N, int64_t lddy, int64_t ldz, int act,
-                                                               int slices) {
-    __shared__ float red[8][kDzCols + 4];
+                                                               int64_t M, int N, int64_t lddy, int64_t ldz, int slices) {
+    __shared__ float red[kDzRows][kDzCols + 4];
     const int chunk = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int col = blockIdx.x * kDzCols + chunk * 8;
     const bool in = col < N;
-    float sum[8];
+    float2 sum[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-    for (int64_t row = (int64_t)blockIdx.y * 8 + rl; in && row < M; row += (int64_t)slices * 8) {
-        float f[8];
-        Chunk<__nv_bfloat16>::unpack(ld_stream(dy + row * lddy + col), f);
-        if (act != QKN_ACT_NONE) {
-            float v[8];
-            Chunk<__nv_bfloat16>::unpack(ld_stream(z + row * ldz + col), v);
+    for (int e = 0; e < 4; ++e) sum[e] = pair_of(0.f);
+    const int64_t step = (int64_t)slices * kDzRows;
+    for (int64_t row0 = (int64_t)blockIdx.y * kDzRows + rl; in && row0 < M; row0 += kDzUnroll * step) {
+        uint4 g[kDzUnroll], v[kDzUnroll];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= slope(act, v[e]);
-            *reinterpret_cast<uint4 *>(dz + row * N + col) = Chunk<__nv_bfloat16>::pack(f);
+        for (int u = 0; u < kDzUnroll; ++u) {
+            const int64_t row = row0 + u * step;
+            g[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < M) {
+                g[u] = ld_stream(dy + row * lddy + col);
+                if constexpr (ACT != QKN_ACT_NONE) v[u] = ld_stream(z + row * ldz + col);
+            }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += f[e];
+        for (int u = 0; u < kDzUnroll; ++u) {
+            const int64_t row = row0 + u * step;
+            if (row >= M) continue;
+            float2 f[4] = {make_float2(bf16lo(g[u].x), bf16hi(g[u].x)), make_float2(bf16lo(g[u].y), bf16hi(g[u].y)),
+                           make_float2(bf16lo(g[u].z), bf16hi(g[u].z)), make_float2(bf16lo(g[u].w), bf16hi(g[u].w))};
+            if constexpr (ACT != QKN_ACT_NONE) {
+                f[0] = __fmul2_rn(f[0], slope2<ACT>(make_float2(bf16lo(v[u].x), bf16hi(v[u].x))));
+                f[1] = __fmul2_rn(f[1], slope2<ACT>(make_float2(bf16lo(v[u].y), bf16hi(v[u].y))));
+                f[2] = __fmul2_rn(f[2], slope2<ACT>(make_float2(bf16lo(v[u].z), bf16hi(v[u].z))));
+                f[3] = __fmul2_rn(f[3], slope2<ACT>(make_float2(bf16lo(v[u].w), bf16hi(v[u].w))));
+                *reinterpret_cast<uint4 *>(dz + row * N + col) =
+                    make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                               pack_bf16x2(f[3].x, f[3].y));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = __fadd2_rn(sum[e], f[e]);
+        }
     }
     if (part == nullptr) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[rl][chunk * 8 + e] = sum[e];
+    for (int e = 0; e < 4; ++e) {
+        red[rl][chunk * 8 + 2 * e] = sum[e].x;
+        red[rl][chunk * 8 + 2 * e + 1] = sum[e].y;
+    }
     __syncthreads();
     const int c = blockIdx.x * kDzCols + threadIdx.x;
     if (c < N) {
         float s = red[0][threadIdx.x];
 #pragma unroll
-        for (int j = 1; j < 8; ++j) s += red[j][threadIdx.x];
+        for (int j = 1; j < kDzRows; ++j) s += red[j][threadIdx.x];
         part[(int64_t)blockIdx.y * N + c] = s;
     }
 }
@@ -90,10 +112,10 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float *__restrict_
     }
 }
 
-// Row slices of the pass: eight 256-thread blocks per SM in all, at least a row group each.
+// Row slices of the pass: about six 256-thread blocks per SM in all, at least a row group each.
 int dz_slices(int64_t M, int64_t N) {
-    const int64_t cols = (N + kDzCols - 1) / kDzCols, groups = (M + 7) / 8;
-    int64_t s = 8 * (int64_t)sm_count() / cols;
+    const int64_t cols = (N + kDzCols - 1) / kDzCols, groups = (M + kDzRows - 1) / kDzRows;
+    int64_t s = 6 * (int64_t)sm_count() / cols;
     if (s < 1) s = 1;
     if (s > groups) s = groups;
     return (int)s;
@@ -103,14 +125,18 @@ size_t dz_bytes(int64_t M, int64_t N, int act) {
     return act == QKN_ACT_NONE ? 0 : ((size_t)M * (size_t)N * 2 + 255) / 256 * 256;
 }
 
-constexpr int kRowsMax = 128;
+template <int ACT>
+qkn_status launch_dz(const __nv_bfloat16 *dy, const __nv_bfloat16 *z, __nv_bfloat16 *dz, float *part, int64_t M, int64_t N,
+                     int64_t lddy, int64_t ldz, int slices, cudaStream_t s) {
+    const dim3 grid((unsigned)((N + kDzCols - 1) / kDzCols), (unsigned)slices);
+    linear_dz_kernel<ACT><<<grid, kDzThreads, 0, s>>>(dy, z, dz, part, M, (int)N, lddy, ldz, slices);
+    return check_launch("linear_dz_kernel launch");
+}
 
 template <int ACT>
 qkn_status forward(const pair::Matrix &x, const pair::Matrix &W, const pair::Matrix &y, const pair::Matrix *res,
                    const pair::Matrix *z, const Epilogue &epi, int64_t K, cudaStream_t s) {
-    int limit = kRowsMax;
-    if (const char *v = getenv("LIN_ROWS_MAX")) limit = atoi(v);
-    if (y.rows <= limit) return rows::launch<ACT>(x, W, y, res, z, epi, K, s);
+    if (rows::takes(y.rows, y.inner, K)) return rows::launch<ACT>(x, W, y, res, z, epi, K, s);
     return pair::launch<false, false, ACT>(x, W, y, res, z, epi, K, s);
 }
 
@@ -227,11 +253,15 @@ extern "C" QKN_API qkn_status linear_fused_backward(const void *dy, const void *
         __nv_bfloat16 *dz = static_cast<__nv_bfloat16 *>(workspace);
         float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + lin::dz_bytes(M, N, act));
         const int slices = lin::dz_slices(M, N);
-        const dim3 grid((unsigned)((N + lin::kDzCols - 1) / lin::kDzCols), (unsigned)slices);
-        lin::linear_dz_kernel<<<grid, lin::kDzThreads, 0, s>>>(g, static_cast<const __nv_bfloat16 *>(preact), dz,
-                                                               dbias != nullptr ? part : nullptr, M, (int)N, lddy, ldz,
-                                                               (int)act, slices);
-        st = check_launch("linear_dz_kernel launch");
+        const __nv_bfloat16 *z = static_cast<const __nv_bfloat16 *>(preact);
+        float *sums = dbias != nullptr ? part : nullptr;
+        switch (act) {
+        case QKN_ACT_RELU: st = lin::launch_dz<QKN_ACT_RELU>(g, z, dz, sums, M, N, lddy, ldz, slices, s); break;
+        case QKN_ACT_SILU: st = lin::launch_dz<QKN_ACT_SILU>(g, z, dz, sums, M, N, lddy, ldz, slices, s); break;
+        case QKN_ACT_GELU: st = lin::launch_dz<QKN_ACT_GELU>(g, z, dz, sums, M, N, lddy, ldz, slices, s); break;
+        case QKN_ACT_GELU_TANH: st = lin::launch_dz<QKN_ACT_GELU_TANH>(g, z, dz, sums, M, N, lddy, ldz, slices, s); break;
+        default: st = lin::launch_dz<QKN_ACT_NONE>(g, z, dz, sums, M, N, lddy, ldz, slices, s);
+        }
         if (st == QKN_OK && dbias != nullptr) {
             lin::linear_db_kernel<<<(unsigned)((N + 31) / 32), 256, 0, s>>>(part, dbias, (int)N, slices);
             st = check_launch("linear_db_kernel launch");

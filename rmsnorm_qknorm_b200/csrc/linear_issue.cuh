@@ -13,6 +13,8 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include "qkn_sync.cuh"
+
 namespace qkn {
 namespace lin {
 

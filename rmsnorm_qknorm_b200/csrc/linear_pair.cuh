@@ -13,13 +13,13 @@
 // Roles per CTA (320 threads): warp 0 moves tiles with TMA, one lane of the
 // even CTA's warp 1 issues the MMAs, warps 2-9 run the epilogue of a tile
 // while the MMAs of the next one run into the other accumulator: a quarter of
-// the rows and half of the columns per warp, a row per thread, 32 columns at
-// a time: accumulator -> times the row's scale, plus bias -> z (stored where
-// asked) -> activation -> plus residual -> y.  Residual, z and y are read and
-// written where they lie, whole 32-byte sectors per thread (16 bytes where
-// the rows are not 32-byte aligned); the residual is asked for before the
-// accumulator is waited for.  (Staged through shared memory and TMA by four
-// warps, a block was a chain of waits: 27 us for a call of one tile.)
+// the rows and half of the columns per warp, a row per thread: accumulator
+// -> times the row's scale, plus bias -> z (stored where asked) -> activation
+// -> plus residual -> y.  y leaves through 32 x 64 boxes in shared memory and
+// TMA stores; the residual comes by TMA into the box that y then overwrites
+// in place, one box ahead.  (Both read and written by the threads, a 32-byte
+// sector of another row per lane, the requests to L2 alone took 2.6 us per
+// tile and operand.)  z, which only training asks for, is written that way.
 // Every wait is bounded and records a failure in g_linear_error.
 #pragma once
 
@@ -30,27 +30,32 @@ constexpr int BM = 128, BK = 64;                   // rows per CTA (256 per pair
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int BAR_BYTES = 256;
+constexpr int BAR_BYTES = 320;
+
+constexpr int BOX_COLS = 64, BOX_BYTES = 32 * BOX_COLS * 2;  // an epilogue warp's staging box: 32 rows
 
 // The tile's columns: 256, or 128 where the wider tiles leave pairs without work.
 template <int BN> struct Shape {
+    static constexpr int EPI_BYTES = EPI_WARPS * 2 * BOX_BYTES;
     static constexpr int BN_CTA = BN / 2;          // rows of B that each CTA loads
     static constexpr int B_BYTES = BN_CTA * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = (226 * 1024 - BAR_BYTES - 1024) / STAGE_BYTES;
+    static constexpr int BIAS_BYTES = BN * 4;
+    static constexpr int STAGES = (227 * 1024 - BAR_BYTES - 1024 - EPI_BYTES - BIAS_BYTES) / STAGE_BYTES;
     static constexpr int PAIR_STAGE_BYTES = 2 * STAGE_BYTES;
     static constexpr int TMEM_COLS = 2 * BN;       // two accumulators
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BAR_BYTES + 1024;
-    static_assert(SMEM_BYTES <= 227 * 1024 && (2 * STAGES + 6) * 8 <= BAR_BYTES, "shared memory budget");
+    static constexpr int BOXES = BN / 2 / BOX_COLS;  // of an epilogue warp, per tile
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + BIAS_BYTES + BAR_BYTES + 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024 && (2 * STAGES + 6 + 2 * EPI_WARPS) * 8 <= BAR_BYTES, "shared memory budget");
 };
 constexpr int GROUP_M = 16;  // pair row blocks walked together down each column block (operands shared in L2)
 
 struct Args {
     Epilogue epi;
-    const __nv_bfloat16 *res;
-    __nv_bfloat16 *y, *z;
-    int64_t ldr, ldy, ldz;
-    int wide;              // residual, z and y rows are 32-byte aligned
+    __nv_bfloat16 *z;
+    int64_t ldz;
+    int wide;              // the rows of z are 32-byte aligned
+    int has_res;
     int M, N;              // of C
     int pm_blocks, n_blocks, k_blocks, num_tiles;
 };
@@ -102,28 +107,10 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *ma
 }
 
 // 16 bf16 of a row, as far as they lie inside it: 32 bytes at once where the rows allow.
-__device__ __forceinline__ void load16(const __nv_bfloat16 *p, bool wide, int left, uint32_t (&w)[8]) {
-    if (wide && left >= 16) {
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "l"(p) : "memory");
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (left > 8 * h) v = *reinterpret_cast<const uint4 *>(p + 8 * h);
-        w[4 * h] = v.x;
-        w[4 * h + 1] = v.y;
-        w[4 * h + 2] = v.z;
-        w[4 * h + 3] = v.w;
-    }
-}
-
-__device__ __forceinline__ void store16(__nv_bfloat16 *p, bool wide, int left, const float (&f)[16]) {
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, bool wide, int left, const float2 *f) {
     uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(f[i].x, f[i].y);
     if (wide && left >= 16) {
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                      ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -138,16 +125,17 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *p, bool wide, int left, c
 template <bool A_MN, bool B_MN, int BN, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                   const Args g) {
+                   const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ CUtensorMap tmap_res, const Args g) {
     using S = Shape<BN>;
     constexpr int STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, BN_CTA = S::BN_CTA;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES + S::EPI_BYTES + S::BIAS_BYTES);
     uint64_t *full = bars, *empty = bars + STAGES;
     uint64_t *acc_full = bars + 2 * STAGES, *acc_empty = bars + 2 * STAGES + 2;
     uint64_t *drained = bars + 2 * STAGES + 4;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 5);
+    uint64_t *res_full = bars + 2 * STAGES + 5;  // [EPI_WARPS][2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(res_full + 2 * EPI_WARPS);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -164,6 +152,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             mbar_init(smem_u32(&acc_empty[a]), 2 * EPI_WARPS);  // even CTA: the epilogue warps of both
         }
         mbar_init(smem_u32(drained), 1);
+        for (int i = 0; i < 2 * EPI_WARPS; ++i) mbar_init(smem_u32(&res_full[i]), 1);
         mbar_init_fence();
     }
     if (warp == 1) {  // whole warp, in both CTAs: the pair's tensor memory
@@ -252,64 +241,131 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
         const int quarter = warp & 3;       // TMEM lanes this warp may access: 32 * quarter ...
         const int half = (warp - 2) >> 2;   // its half of the columns
         const uint32_t acc_empty_leader0 = map_to_rank(smem_u32(&acc_empty[0]), 0);
-        const bool wide = g.wide != 0;
-        int it = 0;
-        for (int tile = pair_id; tile < g.num_tiles; tile += num_pairs, ++it) {
+        const uint32_t boxes = smem_u32(smem + STAGES * STAGE_BYTES) + (uint32_t)(warp - 2) * 2u * BOX_BYTES;
+        const uint32_t rbar = smem_u32(&res_full[2 * (warp - 2)]);
+        float *bias = reinterpret_cast<float *>(smem + STAGES * STAGE_BYTES + S::EPI_BYTES) + half * (BN / 2);
+        const bool wide = g.wide != 0, has_res = g.has_res != 0;
+        uint32_t box = 0, asked = 0;  // boxes stored so far, residual boxes asked for
+        bool ok = true;
+        // corner of this warp's j-th box of a tile; false when it lies outside C
+        auto corner = [&](int tile, int j, int &row0, int &col0) {
             int pm, n;
             tile_coords(tile, g, pm, n);
+            row0 = pm * 2 * BM + (int)rank * BM + quarter * 32;
+            col0 = n * BN + half * (BN / 2) + j * BOX_COLS;
+            return row0 < g.M && col0 < g.N;
+        };
+        // the residual of a box into the buffer its y leaves from; the stores issued so far have
+        // been read by then
+        auto fetch = [&](int row0, int col0) {
+            const uint32_t bar = rbar + (asked & 1u) * 8u;
+            if (lane == 0) {
+                bulk_wait_read0();
+                mbar_arrive_expect_tx(bar, BOX_BYTES);
+                tma_load_2d(boxes + (asked & 1u) * BOX_BYTES, &tmap_res, col0, row0, bar);
+            }
+            ++asked;
+        };
+        int it = 0;
+        // after a wait that gave up (!ok) a warp still meets the others at every barrier
+        for (int tile = pair_id; tile < g.num_tiles; tile += num_pairs, ++it) {
+            int row0, col0;
+            if (corner(tile, 0, row0, col0) && has_res && ok && asked == box) fetch(row0, col0);
             const int acc = it & 1;
             const uint32_t acc_phase = (it >> 1) & 1;
-            const int row = pm * 2 * BM + (int)rank * BM + quarter * 32 + lane;
-            const int col0 = n * BN + half * (BN / 2);
+            const int row = row0 + lane;
             const bool in = row < g.M;
-            const __nv_bfloat16 *res = g.res != nullptr && in ? g.res + row * g.ldr : nullptr;
-            __nv_bfloat16 *y = g.y + row * g.ldy, *z = g.z != nullptr && in ? g.z + row * g.ldz : nullptr;
-            uint32_t q[2][8];
-            if (res != nullptr)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) load16(res + col0 + 16 * h, wide, g.N - col0 - 16 * h, q[h]);
+            __nv_bfloat16 *z = g.z != nullptr && in ? g.z + row * g.ldz : nullptr;
+            // the columns' bias: a value per thread of the half's four warps, which share it
+            asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
+            for (int i = quarter * 32 + lane; i < BN / 2; i += 128) {
+                const int c = col0 + i;
+                float b = 0.f;
+                if (g.epi.bias != nullptr && c < g.N)
+                    b = g.epi.bias_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(g.epi.bias)[c])
+                                        : static_cast<const float *>(g.epi.bias)[c];
+                bias[i] = b;
+            }
             const float r = g.epi.inv_rms != nullptr && in ? __ldg(g.epi.inv_rms + row) : 1.f;
-            if (!mbar_wait(smem_u32(&acc_full[acc]), acc_phase, &g_linear_error)) break;
+            asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
+            if (ok) ok = warp_wait(smem_u32(&acc_full[acc]), acc_phase, &g_linear_error);
             gemm::tc_fence_after();
             const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN + half * (BN / 2);
-#pragma unroll 1
-            for (int c = 0; c < BN / 64; ++c) {
-                const int col = col0 + c * 32;
-                uint32_t v[32];
-                gemm::tmem_ld_32cols(tbase + c * 32, v);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int at = col + 16 * h, left = g.N - at;
-                    float f[16];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float b[8];
-                        if (left > 8 * k) load_bias8(g.epi, at + 8 * k, b);
-                        else
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) b[e] = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[8 * k + e] = fmaf(__uint_as_float(v[16 * h + 8 * k + e]), r, b[e]);
-                    }
-                    if (z != nullptr) store16(z + at, wide, left, f);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = activate<ACT>(f[e]);
-                    if (res != nullptr) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            f[2 * e] += bf16lo(q[h][e]);
-                            f[2 * e + 1] += bf16hi(q[h][e]);
-                        }
-                        // the next block's residual (the bytes of y written here are not among them)
-                        if (c + 1 < BN / 64) load16(res + at + 32, wide, left - 32, q[h]);
-                    }
-                    if (in) store16(y + at, wide, left, f);
+            for (int j = 0; ok && j < S::BOXES; ++j) {
+                const int col = col0 + j * BOX_COLS;
+                if (row0 >= g.M || col >= g.N) break;  // the boxes behind it lie outside, too
+                const uint32_t buf = boxes + (box & 1u) * BOX_BYTES;
+                if (has_res) {
+                    ok = warp_wait(rbar + (box & 1u) * 8u, (box >> 1) & 1u, &g_linear_error);
+                    if (!ok) break;
+                } else if (lane == 0 && box >= 2) {
+                    bulk_wait_read1();  // the store that used this buffer has read it
                 }
+                __syncwarp();
+#pragma unroll 1
+                for (int c = 0; c < BOX_COLS / 32; ++c) {
+                    uint32_t v[32];
+                    gemm::tmem_ld_32cols(tbase + j * BOX_COLS + c * 32, v);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float2 f[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 b = *reinterpret_cast<const float4 *>(bias + j * BOX_COLS + c * 32 + h * 16 + 4 * e);
+                            f[2 * e] = __ffma2_rn(make_float2(__uint_as_float(v[16 * h + 4 * e]), __uint_as_float(v[16 * h + 4 * e + 1])),
+                                                  pair_of(r), make_float2(b.x, b.y));
+                            f[2 * e + 1] = __ffma2_rn(make_float2(__uint_as_float(v[16 * h + 4 * e + 2]), __uint_as_float(v[16 * h + 4 * e + 3])),
+                                                      pair_of(r), make_float2(b.z, b.w));
+                        }
+                        const int at = col + c * 32 + h * 16;
+                        if (z != nullptr) store16(z + at, wide, g.N - at, f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = activate2<ACT>(f[e]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            // 16-byte chunk of the box's 128-byte row, at its place in the 128-byte swizzle
+                            const uint32_t p = buf + (uint32_t)lane * 128u + (uint32_t)(((c * 4 + h * 2 + k) ^ (lane & 7)) * 16);
+                            if (has_res) {
+                                uint4 q;
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(p) : "memory");
+                                f[4 * k] = __fadd2_rn(f[4 * k], make_float2(bf16lo(q.x), bf16hi(q.x)));
+                                f[4 * k + 1] = __fadd2_rn(f[4 * k + 1], make_float2(bf16lo(q.y), bf16hi(q.y)));
+                                f[4 * k + 2] = __fadd2_rn(f[4 * k + 2], make_float2(bf16lo(q.z), bf16hi(q.z)));
+                                f[4 * k + 3] = __fadd2_rn(f[4 * k + 3], make_float2(bf16lo(q.w), bf16hi(q.w)));
+                            }
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                         ::"r"(p), "r"(pack_bf16x2(f[4 * k].x, f[4 * k].y)),
+                                         "r"(pack_bf16x2(f[4 * k + 1].x, f[4 * k + 1].y)),
+                                         "r"(pack_bf16x2(f[4 * k + 2].x, f[4 * k + 2].y)),
+                                         "r"(pack_bf16x2(f[4 * k + 3].x, f[4 * k + 3].y)) : "memory");
+                        }
+                    }
+                    if (has_res && c == 0) {  // the next box's residual, into the other buffer
+                        int r1, c1;
+                        const bool more = j + 1 < S::BOXES && col + BOX_COLS < g.N;
+                        if (more ? corner(tile, j + 1, r1, c1) : tile + num_pairs < g.num_tiles && corner(tile + num_pairs, 0, r1, c1))
+                            fetch(r1, c1);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&tmap_y, buf, col, row0);
+                    bulk_commit();
+                }
+                ++box;
             }
             gemm::tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty_leader0 + (uint32_t)acc * 8u);
         }
+        // no copy into or out of the boxes is in flight at the exit
+        if (lane == 0) {
+            for (; box < asked; ++box) mbar_wait(rbar + (box & 1u) * 8u, (box >> 1) & 1u, &g_linear_error);
+            bulk_wait_all();
+        }
+        __syncwarp();
     }
 
     gemm::tc_fence_before();
@@ -331,10 +387,15 @@ struct Matrix {
 };
 
 template <bool A_MN, bool B_MN, int BN, int ACT>
-qkn_status launch_bn(const Matrix &a, const Matrix &b, Args &g, int64_t K, cudaStream_t s) {
+qkn_status launch_bn(const Matrix &a, const Matrix &b, const Matrix &y, const Matrix *res, Args &g, int64_t K,
+                     cudaStream_t s) {
     using S = Shape<BN>;
     const auto kernel = linear_pair_kernel<A_MN, B_MN, BN, ACT>;
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, ty, tr;
+    if (qkn_status st = make_tmap_pitched(&ty, y.p, y.rows, y.inner, y.pitch, BOX_COLS, 32, 128)) return st;
+    tr = ty;
+    if (res != nullptr)
+        if (qkn_status st = make_tmap_pitched(&tr, res->p, res->rows, res->inner, res->pitch, BOX_COLS, 32, 128)) return st;
     if (qkn_status st = make_tmap_pitched(&ta, a.p, a.rows, a.inner, a.pitch, BK, A_MN ? BK : BM, 128)) return st;
     if (qkn_status st = make_tmap_pitched(&tb, b.p, b.rows, b.inner, b.pitch, BK, B_MN ? BK : S::BN_CTA, 128)) return st;
     g.pm_blocks = (int)(((int64_t)g.M + 2 * BM - 1) / (2 * BM));
@@ -367,9 +428,21 @@ qkn_status launch_bn(const Matrix &a, const Matrix &b, Args &g, int64_t K, cudaS
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, g);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, ty, tr, g);
     if (e != cudaSuccess) return cuda_fail(e, "linear_pair_kernel launch");
     return check_launch("linear_pair_kernel launch");
+}
+
+// About how long the kernel takes, in ns: 4 us, and for every round of tiles over the pairs its
+// products (64 k: 340 ns at 256 columns, 240 ns at 128) or, for short K, its epilogue.  Measured
+// with 512 .. 12288 columns, K 512 .. 12288 and 128 .. 2048 rows, gelu and a residual: within a
+// tenth of it, e.g. 512 x 4096 x 4096 27.6 us (256 columns, 32 of 74 pairs) against 20.7 (128),
+// 2048 x 4096 x 4096 52.8 against 70.2.
+inline int64_t cost(int64_t M, int64_t N, int64_t K, int bn) {
+    const int64_t pairs = sm_count() > 1 ? sm_count() / 2 : 1, kb = (K + BK - 1) / BK;
+    const int64_t tiles = ((M + 2 * BM - 1) / (2 * BM)) * ((N + bn - 1) / bn);
+    const int64_t round = bn == 256 ? std::max<int64_t>(7000, 2500 + 340 * kb) : std::max<int64_t>(4400, 1500 + 240 * kb);
+    return 4000 + (tiles + pairs - 1) / pairs * round;
 }
 
 template <bool A_MN, bool B_MN, int ACT>
@@ -377,21 +450,14 @@ qkn_status launch(const Matrix &a, const Matrix &b, const Matrix &y, const Matri
                   const Epilogue &epi, int64_t K, cudaStream_t s) {
     Args g;
     g.epi = epi;
-    g.y = static_cast<__nv_bfloat16 *>(const_cast<void *>(y.p));
-    g.ldy = y.pitch;
-    g.res = res ? static_cast<const __nv_bfloat16 *>(res->p) : nullptr;
-    g.ldr = res ? res->pitch : 0;
+    g.has_res = res != nullptr;
     g.z = z ? static_cast<__nv_bfloat16 *>(const_cast<void *>(z->p)) : nullptr;
     g.ldz = z ? z->pitch : 0;
-    g.wide = aligned(g.y, 32) && g.ldy % 16 == 0 && aligned(g.res, 32) && g.ldr % 16 == 0 && aligned(g.z, 32) &&
-             g.ldz % 16 == 0;
+    g.wide = aligned(g.z, 32) && g.ldz % 16 == 0;
     g.M = (int)y.rows;
     g.N = (int)y.inner;
-    const int64_t pm = (y.rows + 2 * BM - 1) / (2 * BM), pairs = sm_count() / 2;
-    const int64_t w256 = (pm * ((y.inner + 255) / 256) + pairs - 1) / pairs, w128 = (pm * ((y.inner + 127) / 128) + pairs - 1) / pairs;
-    bool narrow = 8 * w128 < 13 * w256;
-    if (const char *v = getenv("LIN_BN")) narrow = atoi(v) == 128;
-    return narrow ? launch_bn<A_MN, B_MN, 128, ACT>(a, b, g, K, s) : launch_bn<A_MN, B_MN, 256, ACT>(a, b, g, K, s);
+    const bool narrow = cost(g.M, g.N, K, 128) < cost(g.M, g.N, K, 256);
+    return narrow ? launch_bn<A_MN, B_MN, 128, ACT>(a, b, y, res, g, K, s) : launch_bn<A_MN, B_MN, 256, ACT>(a, b, y, res, g, K, s);
 }
 
 }  // namespace pair

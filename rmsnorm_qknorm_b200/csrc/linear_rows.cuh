@@ -103,8 +103,11 @@ __device__ __forceinline__ void finish(const Args &g, uint32_t tile, const float
             for (int e = 0; e < 4; ++e) v[e] = fmaf(v[e], r, bias[e]);
             if (g.z != nullptr)
                 *reinterpret_cast<uint2 *>(g.z + m * g.ldz + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = activate<ACT>(v[e]);
+            const float2 lo = activate2<ACT>(make_float2(v[0], v[1])), hi = activate2<ACT>(make_float2(v[2], v[3]));
+            v[0] = lo.x;
+            v[1] = lo.y;
+            v[2] = hi.x;
+            v[3] = hi.y;
             if (g.res != nullptr) {
                 v[0] += bf16lo(q[u].x);
                 v[1] += bf16hi(q[u].x);
@@ -282,6 +285,20 @@ qkn_status launch_bt(const pair::Matrix &x, const pair::Matrix &W, const Args &a
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tw, tx, a);
     if (e != cudaSuccess) return cuda_fail(e, "linear_rows_kernel launch");
     return check_launch("linear_rows_kernel launch");
+}
+
+// Whether this kernel takes a forward product of M rows: always up to 64, where the weights are
+// the traffic; above while it beats the pair kernel's estimate with its own, 5 us and 480 ns per
+// 64 k of the CTAs that share an SM (of the split that launch_bt finds, to one CTA).  Measured
+// like pair::cost, within a fifth: 256 x 4096 x 4096 19.3 us against 20.6, 128 x 12288 x 4096
+// 36.7 against 32.1, 1024 x 1024 x 1024 9.2 against 9.3, 512 x 4096 x 4096 31.3 against 20.7.
+inline bool takes(int64_t M, int64_t N, int64_t K) {
+    if (M <= 64) return true;
+    const int64_t sms = sm_count(), kb = (K + BK - 1) / BK, tiles = ((N + BF - 1) / BF) * ((M + 127) / 128);
+    int64_t split = std::min<int64_t>(std::min<int64_t>(kMaxCluster, kb / kMinBlocks), 7 * sms / 4 / tiles);
+    if (split < 1) split = 1;
+    const int64_t mine = 5000 + (tiles * split + sms - 1) / sms * ((kb + split - 1) / split) * 480;
+    return mine < std::min(pair::cost(M, N, K, 128), pair::cost(M, N, K, 256));
 }
 
 template <int ACT>

@@ -85,9 +85,12 @@ def check_forward(x, W, bias, act, res, inv, y, z, what=""):
     close(y, yr, ye, what + " y")
 
 
-# from a single token to several tiles; widths of less than a tile, one tile and ragged ones
+# From a single token to several tiles; widths of less than a tile, one tile and ragged ones.  The
+# kernel for few rows serves them up to 700 (16, 32, 64 and 128 tokens per tile, several tiles of
+# 128 at the end, K split and whole), the pair kernel the last two: 128 columns per tile (1029) and 256 (1500).
 SIZES = [(1, 64, 64), (1, 264, 1000), (2, 8, 8), (3, 128, 72), (17, 520, 136), (64, 256, 512), (100, 1032, 264),
-         (128, 128, 128), (129, 264, 1000), (256, 256, 256), (257, 520, 64), (700, 776, 200), (1029, 2056, 1000)]
+         (128, 128, 128), (129, 264, 1000), (256, 256, 256), (257, 520, 64), (700, 776, 200), (1029, 2056, 1000),
+         (1500, 4104, 1600)]
 
 
 @pytest.mark.parametrize("act", ACTS)
