@@ -136,7 +136,8 @@ qkn_status launch_dz(const __nv_bfloat16 *dy, const __nv_bfloat16 *z, __nv_bfloa
 template <int ACT>
 qkn_status forward(const pair::Matrix &x, const pair::Matrix &W, const pair::Matrix &y, const pair::Matrix *res,
                    const pair::Matrix *z, const Epilogue &epi, int64_t K, cudaStream_t s) {
-    if (rows::takes(y.rows, y.inner, K)) return rows::launch<ACT>(x, W, y, res, z, epi, K, s);
+    if (const int tokens = rows::tokens_per_tile(y.rows, y.inner, K))
+        return rows::launch<ACT>(x, W, y, res, z, epi, K, tokens, s);
     return pair::launch<false, false, ACT>(x, W, y, res, z, epi, K, s);
 }
 

@@ -287,23 +287,33 @@ qkn_status launch_bt(const pair::Matrix &x, const pair::Matrix &W, const Args &a
     return check_launch("linear_rows_kernel launch");
 }
 
-// Whether this kernel takes a forward product of M rows: always up to 64, where the weights are
-// the traffic; above while it beats the pair kernel's estimate with its own, 5 us and 480 ns per
-// 64 k of the CTAs that share an SM (of the split that launch_bt finds, to one CTA).  Measured
-// like pair::cost, within a fifth: 256 x 4096 x 4096 19.3 us against 20.6, 128 x 12288 x 4096
-// 36.7 against 32.1, 1024 x 1024 x 1024 9.2 against 9.3, 512 x 4096 x 4096 31.3 against 20.7.
-inline bool takes(int64_t M, int64_t N, int64_t K) {
-    if (M <= 64) return true;
-    const int64_t sms = sm_count(), kb = (K + BK - 1) / BK, tiles = ((N + BF - 1) / BF) * ((M + 127) / 128);
+// About how long the kernel takes with bt tokens per tile, in ns: 3.5 us, and for each of the CTAs
+// that share an SM its blocks of 64 k (c below) and the 25 ns a token takes in the last step.
+// Measured like pair::cost; it leaves out the weights' way from DRAM, which is the same for
+// every bt and sets the time of few tokens and many features.
+inline int64_t cost(int64_t M, int64_t N, int64_t K, int bt) {
+    const int64_t sms = sm_count(), kb = (K + BK - 1) / BK, tiles = ((N + BF - 1) / BF) * ((M + bt - 1) / bt);
+    const int64_t c = bt == 16 ? 190 : bt == 32 ? 200 : bt == 64 ? 300 : 480;
     int64_t split = std::min<int64_t>(std::min<int64_t>(kMaxCluster, kb / kMinBlocks), 7 * sms / 4 / tiles);
     if (split < 1) split = 1;
-    const int64_t mine = 5000 + (tiles * split + sms - 1) / sms * ((kb + split - 1) / split) * 480;
-    return mine < std::min(pair::cost(M, N, K, 128), pair::cost(M, N, K, 256));
+    return 3500 + (tiles * split + sms - 1) / sms * ((kb + split - 1) / split * c + 25 * std::min<int64_t>(bt, M) / split);
+}
+
+// Tokens per tile for a forward product of M rows, 0 where the pair kernel is estimated faster.
+// Up to 64 rows, where the weights are the traffic, this kernel always serves; e.g. 256 x 4096 x
+// 4096 19.3 us against 20.6 by the pair kernel, 128 x 12288 x 4096 36.7 against 32.1, 1024 x 1024
+// x 1024 9.2 against 9.3, 512 x 4096 x 4096 31.3 against 20.7.
+inline int tokens_per_tile(int64_t M, int64_t N, int64_t K) {
+    int best = 16;
+    for (int bt = 32; bt <= 128; bt *= 2)
+        if (cost(M, N, K, bt) < cost(M, N, K, best)) best = bt;
+    if (M > 64 && cost(M, N, K, best) >= std::min(pair::cost(M, N, K, 128), pair::cost(M, N, K, 256))) return 0;
+    return best;
 }
 
 template <int ACT>
 qkn_status launch(const pair::Matrix &x, const pair::Matrix &W, const pair::Matrix &y, const pair::Matrix *res,
-                  const pair::Matrix *z, const Epilogue &epi, int64_t K, cudaStream_t s) {
+                  const pair::Matrix *z, const Epilogue &epi, int64_t K, int tokens, cudaStream_t s) {
     Args a;
     a.epi = epi;
     a.res = res ? static_cast<const __nv_bfloat16 *>(res->p) : nullptr;
@@ -315,9 +325,9 @@ qkn_status launch(const pair::Matrix &x, const pair::Matrix &W, const pair::Matr
     a.M = (int)y.rows;
     a.N = (int)y.inner;
     a.k_blocks = (int)((K + BK - 1) / BK);
-    if (a.M <= 16) return launch_bt<16, ACT>(x, W, a, s);
-    if (a.M <= 32) return launch_bt<32, ACT>(x, W, a, s);
-    if (a.M <= 64) return launch_bt<64, ACT>(x, W, a, s);
+    if (tokens == 16) return launch_bt<16, ACT>(x, W, a, s);
+    if (tokens == 32) return launch_bt<32, ACT>(x, W, a, s);
+    if (tokens == 64) return launch_bt<64, ACT>(x, W, a, s);
     return launch_bt<128, ACT>(x, W, a, s);
 }
 
