@@ -29,6 +29,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -673,16 +674,36 @@ def _row_outputs(q, k, q_out, k_out, inplace: bool, stream):
     return *_result(q, q_out, "q_out", stream), *(_result(k, k_out, "k_out", stream) if k is not None else (None, None, 0))
 
 
-def _call(fn: str, dev: torch.device, *args, stream) -> None:
-    """lib.fn(*args, stream) with the data's device current."""
-    lib = load_library()
-    if torch.cuda.current_device() == dev.index:
-        st = getattr(lib, fn)(*args, _stream(stream))
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_entry = {}  # C entry points by name, once the library is loaded
+
+
+def _call(name: str, dev: torch.device, args: tuple, stream, given: tuple) -> None:
+    """lib.name(*args, stream) with the data's device current.
+
+    ``given`` are the (name, tensor or None) pairs of the call, which all have
+    to live on ``dev``.
+    """
+    index = dev.index
+    for _, t in given:
+        if t is not None and t.get_device() != index:
+            _device_mismatch(dev, given)
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(load_library(), name)
+    if _get_device() == index:
+        st = fn(*args, _raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream))
     else:
         with _On(dev):
-            st = getattr(lib, fn)(*args, _stream(stream))
+            st = fn(*args, _stream(stream))
     if st != 0:
-        _check(fn, st)
+        _check(name, st)
+
+
+def _device_mismatch(dev: torch.device, given: tuple) -> None:
+    for name, t in given:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device} but the call's inputs are on {dev}")
 
 
 def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -704,9 +725,10 @@ def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     act = _dtype_code(q.dtype)
     rot = _rotary_args(positions, inv_freq, head_dim, layout, T)
     q_out, qp, ldq_o, k_out, kp, ldk_o = _row_outputs(q, k, q_out, k_out, inplace, stream)
-    dev = _device(q, k=k, positions=positions, inv_freq=inv_freq, q_out=q_out, k_out=k_out)
-    _call("rotary_apply", dev, q.data_ptr(), k.data_ptr() if k is not None else None, qp, kp, T, dq, dk, ldq, ldk,
-          ldq_o, ldk_o, *rot, mscale, 1 if inverse else 0, act, stream=stream)
+    _call("rotary_apply", q.device,
+          (q.data_ptr(), k.data_ptr() if k is not None else None, qp, kp, T, dq, dk, ldq, ldk, ldq_o, ldk_o, *rot, mscale,
+           1 if inverse else 0, act), stream,
+          (("k", k), ("positions", positions), ("inv_freq", inv_freq), ("q_out", q_out), ("k_out", k_out)))
     return q_out, k_out
 
 
@@ -728,17 +750,24 @@ def qknorm_rotary(q: torch.Tensor, k: torch.Tensor | None, wq: torch.Tensor, wk:
     wdt = _pair_weights(wq, wk, dq, dk, has_k)
     rot = _rotary_args(positions, inv_freq, head_dim, layout, T) if inv_freq is not None else _NO_ROTARY
     q_out, qp, ldq_o, k_out, kp, ldk_o = _row_outputs(q, k, q_out, k_out, inplace, stream)
-    dev = _device(q, k=k, wq=wq, wk=wk if has_k else None, positions=positions if inv_freq is not None else None,
-                  inv_freq=inv_freq, q_out=q_out, k_out=k_out)
-    _call("qknorm_rotary", dev, q.data_ptr(), k.data_ptr() if has_k else None, wq.data_ptr(),
-          wk.data_ptr() if has_k else None, qp, kp, T, dq, dk, ldq, ldk, ldq_o, ldk_o, *rot, mscale, act, wdt, eps,
-          stream=stream)
+    _call("qknorm_rotary", q.device,
+          (q.data_ptr(), k.data_ptr() if has_k else None, wq.data_ptr(), wk.data_ptr() if has_k else None, qp, kp, T, dq,
+           dk, ldq, ldk, ldq_o, ldk_o, *rot, mscale, act, wdt, eps), stream,
+          (("k", k), ("wq", wq), ("wk", wk if has_k else None),
+           ("positions", positions if inv_freq is not None else None), ("inv_freq", inv_freq), ("q_out", q_out),
+           ("k_out", k_out)))
     return q_out, k_out
 
 
 def qknorm_rotary_backward_workspace_bytes(T: int, dq: int, dk: int) -> int:
     """Device scratch qknorm_rotary_backward needs for these sizes (bytes)."""
     return int(load_library().qknorm_rotary_backward_workspace_bytes(T, dq, dk))
+
+
+@functools.lru_cache(maxsize=256)
+def _rotary_workspace(dev: torch.device, T: int, dq: int, dk: int) -> int:
+    with _On(dev):  # the size goes by the device's number of SMs
+        return qknorm_rotary_backward_workspace_bytes(T, dq, dk)
 
 
 def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.Tensor, k: torch.Tensor | None,
@@ -769,28 +798,28 @@ def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.T
     wdt = _pair_weights(wq, wk, dq, dk, has_k)
     rot = _rotary_args(positions, inv_freq, head_dim, layout, T) if inv_freq is not None else _NO_ROTARY
     dq_t, qp, ld_dq, dk_t, kp, ld_dk = _row_outputs(q, k, dq_out, dk_out, False, stream)
-    with _AllocOn(stream, q.device):
+    dev = q.device
+    with _AllocOn(stream, dev):
         if dwq_out is None:
-            dwq_out = torch.empty(dq, dtype=torch.float32, device=q.device)
+            dwq_out = torch.empty(dq, dtype=torch.float32, device=dev)
         if has_k and dwk_out is None:
-            dwk_out = torch.empty(dk, dtype=torch.float32, device=q.device)
+            dwk_out = torch.empty(dk, dtype=torch.float32, device=dev)
         if workspace is None:
-            with _On(q.device):  # the size goes by the device's number of SMs
-                need = load_library().qknorm_rotary_backward_workspace_bytes(T, dq, dk)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(_rotary_workspace(dev, T, dq, dk), dtype=torch.uint8, device=dev)
     for name, t, n in (("dwq_out", dwq_out, dq), ("dwk_out", dwk_out if has_k else None, dk)):
         if t is not None:
             _vec(t, name, n)
             if t.dtype != torch.float32:
                 raise ValueError(f"{name} must be fp32")
     _cuda(workspace, "workspace")
-    dev = _device(q, gq=gq, k=k, gk=gk, wq=wq, wk=wk if has_k else None,
-                  positions=positions if inv_freq is not None else None, inv_freq=inv_freq, dq_out=dq_t, dk_out=dk_t,
-                  dwq_out=dwq_out, dwk_out=dwk_out if has_k else None, workspace=workspace)
-    _call("qknorm_rotary_backward", dev, gq.data_ptr(), gk.data_ptr() if has_k else None, q.data_ptr(),
-          k.data_ptr() if has_k else None, wq.data_ptr(), wk.data_ptr() if has_k else None, qp, kp, dwq_out.data_ptr(),
-          dwk_out.data_ptr() if has_k else None, T, dq, dk, ldgq, ldgk, ldq, ldk, ld_dq, ld_dk, *rot, mscale, act, wdt,
-          eps, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+    _call("qknorm_rotary_backward", dev,
+          (gq.data_ptr(), gk.data_ptr() if has_k else None, q.data_ptr(), k.data_ptr() if has_k else None,
+           wq.data_ptr(), wk.data_ptr() if has_k else None, qp, kp, dwq_out.data_ptr(),
+           dwk_out.data_ptr() if has_k else None, T, dq, dk, ldgq, ldgk, ldq, ldk, ld_dq, ld_dk, *rot, mscale, act, wdt,
+           eps, workspace.data_ptr(), workspace.numel() * workspace.element_size()), stream,
+          (("gq", gq), ("k", k), ("gk", gk), ("wq", wq), ("wk", wk if has_k else None),
+           ("positions", positions if inv_freq is not None else None), ("inv_freq", inv_freq), ("dq_out", dq_t),
+           ("dk_out", dk_t), ("dwq_out", dwq_out), ("dwk_out", dwk_out if has_k else None), ("workspace", workspace)))
     return dq_t, dk_t, dwq_out, (dwk_out if has_k else None)
 
 
@@ -819,9 +848,11 @@ def _bf16_like(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
     return ld
 
 
-def _new(rows: int, cols: int, dtype: torch.dtype, dev: torch.device, stream) -> torch.Tensor:
-    with _AllocOn(stream, dev):
-        return torch.empty((rows, cols), dtype=dtype, device=dev)
+def _new(like: torch.Tensor, rows: int, cols: int, stream) -> torch.Tensor:
+    if stream is None:
+        return like.new_empty((rows, cols))
+    with _AllocOn(stream, like.device):
+        return like.new_empty((rows, cols))
 
 
 def linear_fused(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
@@ -853,21 +884,29 @@ def linear_fused(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = N
             raise ValueError("inv_rms must be fp32")
     ldz = _bf16_like(preact_out, "preact_out", M, N) if preact_out is not None else 0
     if out is None:
-        out, ldy = _new(M, N, torch.bfloat16, x.device, stream), N
+        out, ldy = _new(x, M, N, stream), N
     else:
         ldy = _bf16_like(out, "out", M, N)
-    dev = _device(x, W=W, bias=bias, residual=residual, inv_rms=inv_rms, preact_out=preact_out, out=out)
-    _call("linear_fused", dev, x.data_ptr(), W.data_ptr(), out.data_ptr(), M, N, K, ldx, ldw, ldy,
-          bias.data_ptr() if bias is not None else None, bias_dt, code,
-          residual.data_ptr() if residual is not None else None, ldr,
-          inv_rms.data_ptr() if inv_rms is not None else None,
-          preact_out.data_ptr() if preact_out is not None else None, ldz, stream=stream)
+    _call("linear_fused", x.device,
+          (x.data_ptr(), W.data_ptr(), out.data_ptr(), M, N, K, ldx, ldw, ldy,
+           bias.data_ptr() if bias is not None else None, bias_dt, code,
+           residual.data_ptr() if residual is not None else None, ldr,
+           inv_rms.data_ptr() if inv_rms is not None else None,
+           preact_out.data_ptr() if preact_out is not None else None, ldz), stream,
+          (("W", W), ("bias", bias), ("residual", residual), ("inv_rms", inv_rms), ("preact_out", preact_out),
+           ("out", out)))
     return out
 
 
 def linear_fused_backward_workspace_bytes(M: int, N: int, K: int, act: str = "none") -> int:
     """Device scratch linear_fused_backward needs for these sizes (bytes)."""
     return int(load_library().linear_fused_backward_workspace_bytes(M, N, K, _activation(act)))
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_workspace(dev: torch.device, M: int, N: int, K: int, code: int) -> int:
+    with _On(dev):  # the size goes by the device's number of SMs
+        return int(load_library().linear_fused_backward_workspace_bytes(M, N, K, code))
 
 
 def linear_fused_backward(dy: torch.Tensor, x: torch.Tensor | None, W: torch.Tensor | None,
@@ -905,14 +944,14 @@ def linear_fused_backward(dy: torch.Tensor, x: torch.Tensor | None, W: torch.Ten
     lddx = lddw = 0
     if W is not None:
         if dx_out is None:
-            dx_out, lddx = _new(M, K, torch.bfloat16, dy.device, stream), K
+            dx_out, lddx = _new(dy, M, K, stream), K
         else:
             lddx = _bf16_like(dx_out, "dx_out", M, K)
     elif dx_out is not None:
         raise ValueError("dx_out needs W")
     if x is not None:
         if dW_out is None:
-            dW_out, lddw = _new(N, K, torch.bfloat16, dy.device, stream), K
+            dW_out, lddw = _new(dy, N, K, stream), K
         else:
             lddw = _bf16_like(dW_out, "dW_out", N, K)
     elif dW_out is not None:
@@ -921,17 +960,17 @@ def linear_fused_backward(dy: torch.Tensor, x: torch.Tensor | None, W: torch.Ten
         if need_dbias and dbias_out is None:
             dbias_out = torch.empty(N, dtype=torch.float32, device=dy.device)
         if workspace is None:
-            with _On(dy.device):  # the size goes by the device's number of SMs
-                need = load_library().linear_fused_backward_workspace_bytes(M, N, K, code)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dy.device)
+            workspace = torch.empty(_linear_workspace(dy.device, M, N, K, code), dtype=torch.uint8, device=dy.device)
     _cuda(workspace, "workspace")
     if dbias_out is not None:
         _vec(dbias_out, "dbias_out", N)
         if dbias_out.dtype != torch.float32:
             raise ValueError("dbias_out must be fp32")
-    dev = _device(dy, x=x, W=W, preact=preact, dx_out=dx_out, dW_out=dW_out, dbias_out=dbias_out, workspace=workspace)
     ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-    _call("linear_fused_backward", dev, dy.data_ptr(), ptr(preact), ptr(x), ptr(W), ptr(dx_out), ptr(dW_out),
-          ptr(dbias_out), M, N, K, lddy, ldz, ldx if x is not None else 0, ldw if W is not None else 0, lddx, lddw, code,
-          workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+    _call("linear_fused_backward", dy.device,
+          (dy.data_ptr(), ptr(preact), ptr(x), ptr(W), ptr(dx_out), ptr(dW_out), ptr(dbias_out), M, N, K, lddy, ldz,
+           ldx if x is not None else 0, ldw if W is not None else 0, lddx, lddw, code, workspace.data_ptr(),
+           workspace.numel() * workspace.element_size()), stream,
+          (("x", x), ("W", W), ("preact", preact), ("dx_out", dx_out), ("dW_out", dW_out), ("dbias_out", dbias_out),
+           ("workspace", workspace)))
     return dx_out, dW_out, dbias_out
