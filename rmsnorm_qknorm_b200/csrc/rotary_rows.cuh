@@ -221,6 +221,15 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// The sum of a over the warp on lanes 0 .. 15, of b on lanes 16 .. 31: each half hands the other
+// what it does not keep, then both reduce at once.
+__device__ __forceinline__ float warp_sum_of_two(float a, float b, int lane) {
+    const bool upper = lane & 16;
+    float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+    for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
 // Threads of a block: 20 warps leave a thread 96 registers, 16 warps 128 (the
 // gradients, and the variant with twice the units).
 template <int MODE, int UPT, int E> constexpr int max_threads() { return MODE == kNormBack || UPT * E > 16 ? 512 : 640; }
@@ -406,7 +415,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
             const bool ok = mbar_wait_fast(full + 8u * stage, phase, &g_rotary_error, a.wait_ns);
             const uint32_t src = ring + (uint32_t)(stage * a.stage_bytes);
             const uint32_t tab_s = tables + (uint32_t)(stage * tbytes);
-            float2 va[UPT][H], vb[UPT][H];  // rotary: x; with the norm: x w; gradients: dy turned back
+            float2 va[UPT][H], vb[UPT][H];  // rotary: x; with the norm: x w; gradients: g, dy turned back
             float2 sq[2] = {both(0.f), both(0.f)}, pg[2] = {both(0.f), both(0.f)};  // sums of x^2 and of w g x
             Turns<H> cs;
             if (BACK && same && tab[0] >= 0) cs.load(tab_s + tab[0], run, sin_off);
@@ -468,17 +477,23 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
             float inv_q = 1.f, inv_k = 1.f, cq = 0.f, ck = 0.f;
             bool failed = !ok;
             if constexpr (NORM) {
-                float s = warp_sum(sq[0].x + sq[0].y), t = BACK ? warp_sum(pg[0].x + pg[0].y) : 0.f;
+                float s, t = 0.f;
                 if constexpr (MIXED) {
+                    s = warp_sum(sq[0].x + sq[0].y);
+                    if (BACK) t = warp_sum(pg[0].x + pg[0].y);
                     inv_k = rsqrtf(warp_sum(sq[1].x + sq[1].y) / d_k + a.eps);
                     if (BACK) ck = inv_k * inv_k * (warp_sum(pg[1].x + pg[1].y) / d_k);
                     failed = __any_sync(0xffffffffu, failed);
                 } else {
                     // the sums of this token: [q | k][x^2 | w g x][kSlots], slots without a warp hold zero
                     float *slot = red + (par * 4 + (wk ? 2 : 0)) * kSlots;
-                    if (lane == 0) {
-                        slot[my_warp] = s;
-                        if (BACK) slot[kSlots + my_warp] = t;
+                    if constexpr (BACK) {
+                        // both sums in one pass: the lower lanes end with the first, the upper with the second
+                        const float u = warp_sum_of_two(sq[0].x + sq[0].y, pg[0].x + pg[0].y, lane);
+                        if ((lane & 15) == 0) slot[(lane ? kSlots : 0) + my_warp] = u;
+                    } else {
+                        s = warp_sum(sq[0].x + sq[0].y);
+                        if (lane == 0) slot[my_warp] = s;
                     }
                     failed = group_sync_or(failed, group, a.warps);
                     s = t = 0.f;
@@ -630,12 +645,14 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
     p.rot_units = a.r / (2 * E);
     const int u0 = p.job[0].nunits, u1 = a.njobs > 1 ? p.job[1].nunits : 0;
     auto warps_of = [](int units, int upt) { return (units + 32 * upt - 1) / (32 * upt); };
-    // two units of 16 bf16 elements or four of 8 fp32 a thread, twice that for rows too wide
-    // otherwise; rows of both tensors that one warp holds share it
+    // two units of 16 bf16 elements or four of 8 fp32 a thread (the gradients half of that, which
+    // keeps them clear of spills: 142 against 150 us for 16384 x (5120 + 1024) bf16), twice that
+    // for rows too wide otherwise; rows of both tensors that one warp holds share it
     constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
     const int most = MODE == kNormBack ? kUsual : 4;
-    r.upt = kUsual;
+    r.upt = MODE == kNormBack ? kUsual / 2 : kUsual;
     if (a.njobs > 1 && u0 + u1 <= 32 * kUsual) {
+        r.upt = kUsual;
         r.mixed = true;
         r.warps0 = r.warps = 1;
     } else {
@@ -719,6 +736,7 @@ qkn_status launch(const Args &a, bool *taken, int *grid, cudaStream_t s) {
     p.w_bytes = (MODE == kRotate ? 0 : (p.job[0].d + p.job[1].d) * 4) + 16;  // 16 bytes of zeros
     constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
     if (r.mixed) return launch_layout<TA, MODE, kUsual, true>(p, r, a.layout, grid, s, taken);
+    if (r.upt < kUsual) return launch_layout<TA, MODE, kUsual / 2, false>(p, r, a.layout, grid, s, taken);
     if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, false>(p, r, a.layout, grid, s, taken);
     if constexpr (MODE != kNormBack && kUsual < 4)
         return launch_layout<TA, MODE, 4, false>(p, r, a.layout, grid, s, taken);
