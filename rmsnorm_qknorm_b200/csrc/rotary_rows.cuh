@@ -234,7 +234,7 @@ __device__ __forceinline__ float warp_sum_of_two(float a, float b, int lane) {
 // gradients, and the variant with twice the units).
 template <int MODE, int UPT, int E> constexpr int max_threads() { return MODE == kNormBack || UPT * E > 16 ? 512 : 640; }
 
-// MIXED: one warp serves both tensors; otherwise q and k have warps of their own.
+// MIXED: warps serve both tensors (with the norm, one warp); otherwise q and k have warps of their own.
 template <typename TA, int MODE, int UPT, bool HALF, bool MIXED>
 __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rotary_unit_kernel(const Params a) {
     constexpr int E = Chunk<TA>::E, H = E / 2;
@@ -622,7 +622,7 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
             return r;
         if (MODE == kNormBack && (!aligned(j.g, 16) || j.ldg % 16)) return r;
         if (MODE != kRotate && !aligned(j.w, E * w_size < 16 ? E * w_size : 16)) return r;
-                if ((int64_t)j.d * (int64_t)sizeof(TA) > kSmemLimit) return r;
+        if ((int64_t)j.d * (int64_t)sizeof(TA) > kSmemLimit) return r;
         J.x = j.x;
         J.g = j.g;
         J.y = j.y;
@@ -645,23 +645,20 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
     p.rot_units = a.r / (2 * E);
     const int u0 = p.job[0].nunits, u1 = a.njobs > 1 ? p.job[1].nunits : 0;
     auto warps_of = [](int units, int upt) { return (units + 32 * upt - 1) / (32 * upt); };
-    // two units of 16 bf16 elements or four of 8 fp32 a thread (the gradients half of that, which
-    // keeps them clear of spills: 142 against 150 us for 16384 x (5120 + 1024) bf16), twice that
-    // for rows too wide otherwise; rows of both tensors that one warp holds share it
+    // Two units of 16 bf16 elements or four of 8 fp32 a thread; half of that for the gradients,
+    // which keeps them clear of spills (142 against 150 us for 16384 x (5120 + 1024) bf16);
+    // twice that for rows too wide otherwise.  Warps serve both tensors where nothing is summed
+    // over a row, or where one warp is enough.
     constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
     const int most = MODE == kNormBack ? kUsual : 4;
     r.upt = MODE == kNormBack ? kUsual / 2 : kUsual;
-    if (a.njobs > 1 && u0 + u1 <= 32 * kUsual) {
-        r.upt = kUsual;
-        r.mixed = true;
-        r.warps0 = r.warps = 1;
-    } else {
-        for (;; r.upt *= 2) {
-            if (r.upt > most) return r;
-            r.warps0 = warps_of(u0, r.upt);
-            r.warps = r.warps0 + warps_of(u1, r.upt);
-            if (r.warps <= kMaxWarps) break;
-        }
+    r.mixed = MODE == kRotate || (a.njobs > 1 && u0 + u1 <= 32 * kUsual);
+    if (r.mixed && MODE != kRotate) r.upt = kUsual;
+    for (;; r.upt *= 2) {
+        if (r.upt > most) return r;
+        r.warps0 = r.mixed ? warps_of(u0 + u1, r.upt) : warps_of(u0, r.upt);
+        r.warps = r.mixed ? r.warps0 : r.warps0 + warps_of(u1, r.upt);
+        if (r.warps <= kMaxWarps) break;
     }
     // groups side by side in a block (one block per SM, so that they share the weights' copy)
     r.groups = (MODE == kNormBack || r.upt * E > 16 ? 16 : 20) / (r.warps + 1);
@@ -735,11 +732,16 @@ qkn_status launch(const Args &a, bool *taken, int *grid, cudaStream_t s) {
     p.w_bf16 = sizeof(TW) == 2;
     p.w_bytes = (MODE == kRotate ? 0 : (p.job[0].d + p.job[1].d) * 4) + 16;  // 16 bytes of zeros
     constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
-    if (r.mixed) return launch_layout<TA, MODE, kUsual, true>(p, r, a.layout, grid, s, taken);
-    if (r.upt < kUsual) return launch_layout<TA, MODE, kUsual / 2, false>(p, r, a.layout, grid, s, taken);
-    if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, false>(p, r, a.layout, grid, s, taken);
-    if constexpr (MODE != kNormBack && kUsual < 4)
-        return launch_layout<TA, MODE, 4, false>(p, r, a.layout, grid, s, taken);
+    if constexpr (MODE == kRotate) {
+        if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, true>(p, r, a.layout, grid, s, taken);
+        if constexpr (kUsual < 4) return launch_layout<TA, MODE, 4, true>(p, r, a.layout, grid, s, taken);
+    } else {
+        if (r.mixed) return launch_layout<TA, MODE, kUsual, true>(p, r, a.layout, grid, s, taken);
+        if constexpr (MODE == kNormBack)
+            if (r.upt < kUsual) return launch_layout<TA, MODE, kUsual / 2, false>(p, r, a.layout, grid, s, taken);
+        if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, false>(p, r, a.layout, grid, s, taken);
+        if constexpr (MODE == kNorm && kUsual < 4) return launch_layout<TA, MODE, 4, false>(p, r, a.layout, grid, s, taken);
+    }
     return fail(QKN_ERR_UNSUPPORTED, "rotary_unit_kernel: no variant for these rows");
 }
 
