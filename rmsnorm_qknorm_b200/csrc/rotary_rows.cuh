@@ -397,11 +397,12 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
         // a chunk that is not there reads zeros (behind the weights) and stores nothing
         const uint32_t zeros = w_s + (NORM ? (uint32_t)(chunks * E * 4) : 0u);
         // a thread's units lie at the same place of their heads when a head's units divide the
-        // warps' stride (powers of two do): cos and sin are then read once per token
-        bool same = true;
+        // warps' stride (powers of two do): cos and sin are then read once per token (not for the
+        // gradients, which would spill the registers that keeping them takes)
+        bool same = !BACK;
 #pragma unroll
         for (int i = 1; i < UPT; ++i) same = same && (off_a[i] < 0 || tab[i] == tab[0]);
-        same = __all_sync(0xffffffffu, same);
+        if (!BACK) same = __all_sync(0xffffffffu, same);
         const float d_q = (float)a.job[0].d, d_k = (float)a.job[1].d;
         // rows of the results, moved by the chunk's place in a stage
         uint8_t *yq = (wk ? a.job[1].y - a.job[1].row_off : a.job[0].y) + first_token * (wk ? a.job[1].ldy : a.job[0].ldy);
@@ -411,14 +412,15 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
 
         int stage = 0, par = 0;
         uint32_t phase = 0;
-        for (int64_t n = first_token; n < a.T; n += step) {
+        // tokens of this group (fewer than 2^31)
+        for (int left = first_token < a.T ? (int)((a.T - first_token - 1) / step) + 1 : 0; left > 0; --left) {
             const bool ok = mbar_wait_fast(full + 8u * stage, phase, &g_rotary_error, a.wait_ns);
             const uint32_t src = ring + (uint32_t)(stage * a.stage_bytes);
             const uint32_t tab_s = tables + (uint32_t)(stage * tbytes);
             float2 va[UPT][H], vb[UPT][H];  // rotary: x; with the norm: x w; gradients: g, dy turned back
             float2 sq[2] = {both(0.f), both(0.f)}, pg[2] = {both(0.f), both(0.f)};  // sums of x^2 and of w g x
             Turns<H> cs;
-            if (BACK && same && tab[0] >= 0) cs.load(tab_s + tab[0], run, sin_off);
+
 #pragma unroll
             for (int i = 0; i < UPT; ++i) {
                 const uint32_t pa = off_a[i] >= 0 ? src + off_a[i] : zeros, pb = off_b[i] >= 0 ? src + off_b[i] : zeros;
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
                     unpack2<TA, H>(lds128(off_a[i] >= 0 ? pa + a.x_bytes : zeros), va[i]);
                     unpack2<TA, H>(lds128(off_b[i] >= 0 ? pb + a.x_bytes : zeros), vb[i]);
                     if (tab[i] >= 0) {
-                        if (!same) cs.load(tab_s + tab[i], run, sin_off);
+                        cs.load(tab_s + tab[i], run, sin_off);
                         turn<H, HALF, false>(va[i], vb[i], cs, 1.f);
                     }
                     float2 q = both(0.f), r = both(0.f), w[H], x[H];
@@ -645,15 +647,15 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
     p.rot_units = a.r / (2 * E);
     const int u0 = p.job[0].nunits, u1 = a.njobs > 1 ? p.job[1].nunits : 0;
     auto warps_of = [](int units, int upt) { return (units + 32 * upt - 1) / (32 * upt); };
-    // Two units of 16 bf16 elements or four of 8 fp32 a thread; half of that for the gradients,
-    // which keeps them clear of spills (142 against 150 us for 16384 x (5120 + 1024) bf16);
-    // twice that for rows too wide otherwise.  Warps serve both tensors where nothing is summed
-    // over a row, or where one warp is enough.
+    // Two units of 16 bf16 elements or four of 8 fp32 a thread, twice that for rows too wide
+    // otherwise.  (Half of it leaves fewer groups to an SM, and it is the groups that hide one
+    // another's barriers: 16384 x (5120 + 1024) bf16, gradients 145 against 118 us, rotary alone 93
+    // against 67.)  Warps serve both tensors where nothing is summed over a row, or where one warp
+    // is enough.
     constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
     const int most = MODE == kNormBack ? kUsual : 4;
-    r.upt = MODE == kNormBack ? kUsual / 2 : kUsual;
+    r.upt = kUsual;
     r.mixed = MODE == kRotate || (a.njobs > 1 && u0 + u1 <= 32 * kUsual);
-    if (r.mixed && MODE != kRotate) r.upt = kUsual;
     for (;; r.upt *= 2) {
         if (r.upt > most) return r;
         r.warps0 = r.mixed ? warps_of(u0 + u1, r.upt) : warps_of(u0, r.upt);
@@ -737,8 +739,6 @@ qkn_status launch(const Args &a, bool *taken, int *grid, cudaStream_t s) {
         if constexpr (kUsual < 4) return launch_layout<TA, MODE, 4, true>(p, r, a.layout, grid, s, taken);
     } else {
         if (r.mixed) return launch_layout<TA, MODE, kUsual, true>(p, r, a.layout, grid, s, taken);
-        if constexpr (MODE == kNormBack)
-            if (r.upt < kUsual) return launch_layout<TA, MODE, kUsual / 2, false>(p, r, a.layout, grid, s, taken);
         if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, false>(p, r, a.layout, grid, s, taken);
         if constexpr (MODE == kNorm && kUsual < 4) return launch_layout<TA, MODE, 4, false>(p, r, a.layout, grid, s, taken);
     }
