@@ -372,6 +372,7 @@ QKN_API qkn_status flashnorm_proj_noalloc(const void *x, const void *W_folded, v
  * reduction, less than fp32 resolves up to 10^8 radians.  No table is read or
  * kept.
  *
+ * T          below 2^31
  * positions  [T] int32 (pos_bits 32) or int64 (64), any values, in any order
  * inv_freq   [rotary_dim / 2] fp64, radians per position.  Frequencies that
  *            are scaled for longer contexts are given here as they are
@@ -480,8 +481,8 @@ typedef enum {
  * inv_rms   [M] fp32 row scale (flashnorm_inv_rms, with W folded by
  *           flashnorm_fold_weights), or NULL for 1
  * preact    [M][N] bf16, pitch ldz, receives z for linear_fused_backward, or NULL
- * M >= 0, N and K multiples of 8; pitches multiples of 8; x, W, y, bias,
- * residual and preact 16-byte aligned.  One launch, nothing is allocated.
+ * M >= 0, N and K multiples of 8, each below 2^31 - 512; pitches multiples of
+ * 8; x, W, y, bias, residual and preact 16-byte aligned.  One launch, nothing is allocated.
  * A device-side wait that gives up is reported by qkn_check_device.
  */
 QKN_API qkn_status linear_fused(const void *x, const void *W, void *y,

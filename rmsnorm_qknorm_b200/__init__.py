@@ -611,6 +611,30 @@ class _AllocOn:
         return False
 
 
+def _pitched(t: torch.Tensor, name: str):
+    """(rows, width, pitch) of a 2-D tensor whose rows lie apart in memory."""
+    _cuda(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D with unit stride along the row")
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"{name} must be 2-D with unit stride along the row")
+    if rows <= 1:
+        return rows, cols, cols
+    if s0 < cols:
+        raise ValueError(f"{name} has rows that overlap in memory (an expanded tensor?)")
+    return rows, cols, s0
+
+
+def _not_over(out: torch.Tensor, name: str, inputs: tuple) -> None:
+    """A result that the caller gives does not start where an input does."""
+    p = out.data_ptr()
+    for t in inputs:
+        if t is not None and t.data_ptr() == p and out.numel() and t.numel():
+            raise ValueError(f"{name} must not overlap the inputs")
+
+
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _POS_BITS = {torch.int64: 64, torch.int32: 32}
 _NO_ROTARY = (0, None, 64, None, 0, 0)
@@ -634,7 +658,7 @@ def _rotary_args(positions, inv_freq, head_dim: int, layout: str, T: int):
 
 
 def _rows_like(t: torch.Tensor, name: str, q: torch.Tensor, T: int):
-    rows, d, ld = _rows(t, name)
+    rows, d, ld = _pitched(t, name)
     if rows != T or t.dtype != q.dtype:
         raise ValueError(f"{name} must have q's row count and dtype")
     return d, ld
@@ -660,9 +684,10 @@ def _result(t: torch.Tensor, given: torch.Tensor | None, name: str, stream):
             with _AllocOn(stream, t.device):
                 given = torch.empty_like(t, memory_format=torch.contiguous_format)
         return given, given.data_ptr(), t.shape[1]
-    rows, d = t.shape
-    _out2d(given, name, rows, d, t.dtype)
-    return given, given.data_ptr(), max(given.stride(0), d)
+    rows, d, ld = _pitched(given, name)
+    if (rows, d) != tuple(t.shape) or given.dtype != t.dtype:
+        raise ValueError(f"{name} must be a {t.dtype} [{t.shape[0]}, {t.shape[1]}] tensor")
+    return given, given.data_ptr(), ld
 
 
 def _row_outputs(q, k, q_out, k_out, inplace: bool, stream):
@@ -720,7 +745,7 @@ def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     gradient.  Returns ``(q_out, k_out)``; pitches, outputs and ``inplace`` as
     in :func:`qknorm_fused`.
     """
-    T, dq, ldq = _rows(q, "q")
+    T, dq, ldq = _pitched(q, "q")
     dk, ldk = _rows_like(k, "k", q, T) if k is not None else (0, 0)
     act = _dtype_code(q.dtype)
     rot = _rotary_args(positions, inv_freq, head_dim, layout, T)
@@ -743,7 +768,7 @@ def qknorm_rotary(q: torch.Tensor, k: torch.Tensor | None, wq: torch.Tensor, wk:
     rotation out.  Returns ``(q_out, k_out)``; arguments as in
     :func:`qknorm_fused` and :func:`rotary_apply`.
     """
-    T, dq, ldq = _rows(q, "q")
+    T, dq, ldq = _pitched(q, "q")
     has_k = k is not None
     dk, ldk = _rows_like(k, "k", q, T) if has_k else (0, 0)
     act = _dtype_code(q.dtype)
@@ -785,7 +810,7 @@ def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.T
     at least ``qknorm_rotary_backward_workspace_bytes``) avoids an allocation
     inside the call.
     """
-    T, dq, ldq = _rows(q, "q")
+    T, dq, ldq = _pitched(q, "q")
     act = _dtype_code(q.dtype)
     has_k = k is not None
     if has_k != (gk is not None):
@@ -797,6 +822,9 @@ def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.T
         raise ValueError("gq and gk must have the widths of q and k")
     wdt = _pair_weights(wq, wk, dq, dk, has_k)
     rot = _rotary_args(positions, inv_freq, head_dim, layout, T) if inv_freq is not None else _NO_ROTARY
+    for given, name in ((dq_out, "dq_out"), (dk_out, "dk_out")):
+        if given is not None:
+            _not_over(given, name, (q, k, gq, gk))
     dq_t, qp, ld_dq, dk_t, kp, ld_dk = _row_outputs(q, k, dq_out, dk_out, False, stream)
     dev = q.device
     with _AllocOn(stream, dev):
@@ -834,11 +862,10 @@ def _activation(act: str) -> int:
 
 
 def _bf16_rows(t: torch.Tensor, name: str):
-    rows, cols, ld = _rows(t, name)
+    r = _pitched(t, name)
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bf16")
-    # a single row has no pitch of its own
-    return rows, cols, ld if rows > 1 else (cols + 7) // 8 * 8
+    return r
 
 
 def _bf16_like(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
@@ -887,6 +914,7 @@ def linear_fused(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = N
         out, ldy = _new(x, M, N, stream), N
     else:
         ldy = _bf16_like(out, "out", M, N)
+        _not_over(out, "out", (x, W, preact_out))
     _call("linear_fused", x.device,
           (x.data_ptr(), W.data_ptr(), out.data_ptr(), M, N, K, ldx, ldw, ldy,
            bias.data_ptr() if bias is not None else None, bias_dt, code,
@@ -947,6 +975,7 @@ def linear_fused_backward(dy: torch.Tensor, x: torch.Tensor | None, W: torch.Ten
             dx_out, lddx = _new(dy, M, K, stream), K
         else:
             lddx = _bf16_like(dx_out, "dx_out", M, K)
+            _not_over(dx_out, "dx_out", (dy, W, x, preact))
     elif dx_out is not None:
         raise ValueError("dx_out needs W")
     if x is not None:
@@ -954,6 +983,7 @@ def linear_fused_backward(dy: torch.Tensor, x: torch.Tensor | None, W: torch.Ten
             dW_out, lddw = _new(dy, N, K, stream), K
         else:
             lddw = _bf16_like(dW_out, "dW_out", N, K)
+            _not_over(dW_out, "dW_out", (dy, W, x, preact))
     elif dW_out is not None:
         raise ValueError("dW_out needs x")
     with _AllocOn(stream, dy.device):

@@ -159,12 +159,15 @@ qkn_status read_linear_error(int *flag) {
 
 using namespace qkn;
 
+// Rows and columns at most, so that a tile behind the last one still has 32-bit coordinates.
+static constexpr int64_t kMaxSize = 0x7ffffe00LL;
+
 extern "C" QKN_API qkn_status linear_fused(const void *x, const void *W, void *y, int64_t M, int64_t N, int64_t K,
                                            int64_t ldx, int64_t ldw, int64_t ldy, const void *bias, qkn_dtype bias_dt,
                                            qkn_activation act, const void *residual, int64_t ldr, const float *inv_rms,
                                            void *preact, int64_t ldz, void *stream) {
     const char *fn = "linear_fused";
-    if (M < 0 || N < 1 || K < 1 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL)
+    if (M < 0 || N < 1 || K < 1 || M > kMaxSize || N > kMaxSize || K > kMaxSize)
         return fail(QKN_ERR_SHAPE, "%s: bad sizes M=%lld N=%lld K=%lld", fn, (long long)M, (long long)N, (long long)K);
     if (K % 8 != 0 || N % 8 != 0)
         return fail(QKN_ERR_SHAPE, "%s: K=%lld and N=%lld must be multiples of 8", fn, (long long)K, (long long)N);
@@ -197,7 +200,7 @@ extern "C" QKN_API qkn_status linear_fused(const void *x, const void *W, void *y
 }
 
 extern "C" QKN_API size_t linear_fused_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, qkn_activation act) {
-    if (M < 0 || N < 1 || K < 1 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL || (int)act < QKN_ACT_NONE ||
+    if (M < 0 || N < 1 || K < 1 || M > kMaxSize || N > kMaxSize || K > kMaxSize || (int)act < QKN_ACT_NONE ||
         (int)act > QKN_ACT_GELU_TANH)
         return 0;
     return lin::dz_bytes(M, N, act) + (M ? (size_t)lin::dz_slices(M, N) * (size_t)N * 4 : 0) + 16;
@@ -209,7 +212,7 @@ extern "C" QKN_API qkn_status linear_fused_backward(const void *dy, const void *
                                                     int64_t lddw, qkn_activation act, void *workspace,
                                                     size_t workspace_bytes, void *stream) {
     const char *fn = "linear_fused_backward";
-    if (M < 0 || N < 1 || K < 1 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL)
+    if (M < 0 || N < 1 || K < 1 || M > kMaxSize || N > kMaxSize || K > kMaxSize)
         return fail(QKN_ERR_SHAPE, "%s: bad sizes M=%lld N=%lld K=%lld", fn, (long long)M, (long long)N, (long long)K);
     if (K % 8 != 0 || N % 8 != 0)
         return fail(QKN_ERR_SHAPE, "%s: K=%lld and N=%lld must be multiples of 8", fn, (long long)K, (long long)N);

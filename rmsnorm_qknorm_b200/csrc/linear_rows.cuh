@@ -307,6 +307,7 @@ inline int tokens_per_tile(int64_t M, int64_t N, int64_t K) {
     int best = 16;
     for (int bt = 32; bt <= 128; bt *= 2)
         if (cost(M, N, K, bt) < cost(M, N, K, best)) best = bt;
+    if ((M + best - 1) / best > 65535) return 0;  // the grid's second dimension
     if (M > 64 && cost(M, N, K, best) >= std::min(pair::cost(M, N, K, 128), pair::cost(M, N, K, 256))) return 0;
     return best;
 }

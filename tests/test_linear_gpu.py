@@ -257,3 +257,21 @@ def test_other_stream_graph_and_two_calls_at_once(cuda_lib, M):
     for o in got:
         assert all(torch.equal(p, q) for p, q in zip(o, fresh))
     assert qk.load_library().qkn_check_device(None) == 0
+
+
+def test_refusals_of_the_binding(cuda_lib):
+    x, W, b, z = normal(4, 64), normal(32, 64), normal(32), normal(4, 32)
+    for kw in (dict(x=x[:1].expand(4, -1)), dict(W=W[:, :32]), dict(bias=b[:16]), dict(act="tanh"), dict(residual=z[:1]),
+               dict(residual=z[:1].expand(4, -1)), dict(residual=z.float()), dict(inv_rms=torch.ones(4, device=DEV).bfloat16()),
+               dict(preact_out=z[:, :16]), dict(out=z[:3]), dict(W=W.cpu()), dict(x=x.t()), dict(out=x[:, :32])):
+        a = dict(x=x, W=W) | kw
+        with pytest.raises((ValueError, TypeError)):
+            qk.linear_fused(a.pop("x"), a.pop("W"), **a)
+    with pytest.raises(qk.QKNormError, match="SHAPE"):
+        qk.linear_fused(x[:, :60].contiguous(), W[:, :60].contiguous())
+    with pytest.raises(qk.QKNormError, match="ALIGN"):
+        qk.linear_fused(normal(4, 72)[:, 1:65], W)
+    for args, kw in (((z, x, W, None, "gelu"), {}), ((z, None, None), {}), ((z, x[:3], W), {}),
+                     ((z, x, W), dict(dx_out=z)), ((z, x, None), dict(dx_out=x))):
+        with pytest.raises(ValueError):
+            qk.linear_fused_backward(*args, **kw)

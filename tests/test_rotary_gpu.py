@@ -368,3 +368,25 @@ def test_rows_as_wide_as_the_norm_takes(cuda_lib):
     ref, err, dwr, dwe = norm_back(f64(s["q"]), f64(s["wq"]), g, ge, 1e-6)
     close(got[0], ref, err, torch.float32, "dq")
     close(got[2], dwr, dwe, torch.float32, "dwq")
+
+
+def test_refusals_of_the_binding(cuda_lib):
+    s = make(4, 2, 1, 64, 64, torch.bfloat16, seed=1)
+    d = dev(s)
+    q, k, pos, f = d["q"], d["k"], d["pos"], d["freq"]
+    for bad in (dict(q=q[:1].expand(4, -1)), dict(k=k[:3]), dict(k=k.float()), dict(pos=pos.float()), dict(pos=pos[:3]),
+                dict(f=f.float()), dict(f=None), dict(layout="both"), dict(q_out=q[:, :64]), dict(q=q.t()),
+                dict(q_out=q[:1].expand(4, -1)), dict(inplace=True, q_out=torch.empty_like(q)), dict(f=f.cpu()), dict(pos=pos.cpu())):
+        a = dict(q=q, k=k, pos=pos, f=f) | bad
+        with pytest.raises((ValueError, TypeError)):
+            qk.rotary_apply(a.pop("q"), a.pop("k"), a.pop("pos"), a.pop("f"), 64, **a)
+    with pytest.raises(qk.QKNormError, match="SHAPE"):
+        qk.rotary_apply(q, k, pos, f, 48)
+    back = (d["gq"], d["gk"], q, k, d["wq"], d["wk"], pos, f, 64)
+    for kw in (dict(dq_out=d["gq"]), dict(dq_out=q), dict(dwq_out=torch.empty(128, device=DEV).bfloat16())):
+        with pytest.raises(ValueError):
+            qk.qknorm_rotary_backward(*back, **kw)
+    with pytest.raises(qk.QKNormError, match="workspace"):
+        qk.qknorm_rotary_backward(*back, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError, match="gk"):
+        qk.qknorm_rotary_backward(d["gq"], None, *back[2:])
