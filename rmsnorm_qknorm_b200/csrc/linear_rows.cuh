@@ -160,12 +160,16 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
         // ---------------------------------------------------------------- TMA producer
         int stage = 0;
         uint32_t phase = 0, armed = 0, armed_parity = 0;
+        // every tile of features starts elsewhere in its part of K: the CTAs then read other columns
+        // of W and other parts of x at any one time (12288 x 4096, one token: 21.7 -> 20.8 us)
+        int at = kb0 + (int)(blockIdx.x / ranks) * 5 % (kb1 - kb0);
         for (int kb = kb0; kb < kb1; ++kb) {
             if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, &g_linear_error)) break;
             const uint32_t fb = smem_u32(&full[stage]), sa = smem_u32(smem + stage * STAGE_BYTES);
             elect_expect_tx(fb, STAGE_BYTES);
-            elect_tma_load(sa, &tmap_w, kb * BK, n0, fb);
-            elect_tma_load(sa + W_BYTES, &tmap_x, kb * BK, t0, fb);
+            elect_tma_load(sa, &tmap_w, at * BK, n0, fb);
+            elect_tma_load(sa + W_BYTES, &tmap_x, at * BK, t0, fb);
+            if (++at == kb1) at = kb0;
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
