@@ -20,6 +20,8 @@
 // in place, one box ahead.  (Both read and written by the threads, a 32-byte
 // sector of another row per lane, the requests to L2 alone took 2.6 us per
 // tile and operand.)  z, which only training asks for, is written that way.
+// Eight epilogue warps against sixteen, with gelu and a residual: 2048 x 8192 x
+// 512 31.9 and 29.6 us, 8192 x 12288 x 4096 536 and 575-603.
 // Every wait is bounded and records a failure in g_linear_error.
 #pragma once
 
