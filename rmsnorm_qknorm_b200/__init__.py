@@ -612,19 +612,18 @@ class _AllocOn:
 
 
 def _pitched(t: torch.Tensor, name: str):
-    """(rows, width, pitch) of a 2-D tensor whose rows lie apart in memory."""
-    _cuda(t, name)
-    if t.dim() != 2:
+    """(rows, width, pitch) of a 2-D CUDA tensor whose rows lie apart in memory."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _cuda(t, name)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be 2-D with unit stride along the row")
-    rows, cols = t.shape
-    s0, s1 = t.stride()
-    if cols > 1 and s1 != 1:
-        raise ValueError(f"{name} must be 2-D with unit stride along the row")
+    rows, cols = shape
     if rows <= 1:
         return rows, cols, cols
-    if s0 < cols:
+    if stride[0] < cols:
         raise ValueError(f"{name} has rows that overlap in memory (an expanded tensor?)")
-    return rows, cols, s0
+    return rows, cols, stride[0]
 
 
 def _not_over(out: torch.Tensor, name: str, inputs: tuple) -> None:
@@ -646,7 +645,7 @@ def _rotary_args(positions, inv_freq, head_dim: int, layout: str, T: int):
     if lay is None:
         raise ValueError(f"layout must be 'half' or 'interleaved', not {layout!r}")
     _cuda(inv_freq, "inv_freq")
-    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
+    if inv_freq.dim() != 1 or inv_freq.dtype is not torch.float64 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous 1-D float64 tensor")
     if positions is None:
         raise ValueError("positions is required with inv_freq")
@@ -675,14 +674,17 @@ def _pair_weights(wq, wk, dq: int, dk: int, has_k: bool) -> int:
     return _dtype_code(wq.dtype)
 
 
+_empty_like, _CONTIGUOUS = torch.empty_like, torch.contiguous_format
+
+
 def _result(t: torch.Tensor, given: torch.Tensor | None, name: str, stream):
     """The output that takes the rows of t, its pointer and pitch: the one given, or a new contiguous one."""
     if given is None:
         if stream is None:
-            given = torch.empty_like(t, memory_format=torch.contiguous_format)
+            given = _empty_like(t, memory_format=_CONTIGUOUS)
         else:
             with _AllocOn(stream, t.device):
-                given = torch.empty_like(t, memory_format=torch.contiguous_format)
+                given = _empty_like(t, memory_format=_CONTIGUOUS)
         return given, given.data_ptr(), t.shape[1]
     rows, d, ld = _pitched(given, name)
     if (rows, d) != tuple(t.shape) or given.dtype != t.dtype:
@@ -789,6 +791,17 @@ def qknorm_rotary_backward_workspace_bytes(T: int, dq: int, dk: int) -> int:
     return int(load_library().qknorm_rotary_backward_workspace_bytes(T, dq, dk))
 
 
+def _f32_vector(given: torch.Tensor | None, name: str, like: torch.Tensor) -> torch.Tensor:
+    """The fp32 vector of like's length that takes a result: the one given, or a new one."""
+    n = like.shape[0]
+    if given is None:
+        return like.new_empty(n, dtype=torch.float32)
+    _vec(given, name, n)
+    if given.dtype != torch.float32:
+        raise ValueError(f"{name} must be fp32")
+    return given
+
+
 @functools.lru_cache(maxsize=256)
 def _rotary_workspace(dev: torch.device, T: int, dq: int, dk: int) -> int:
     with _On(dev):  # the size goes by the device's number of SMs
@@ -828,17 +841,10 @@ def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.T
     dq_t, qp, ld_dq, dk_t, kp, ld_dk = _row_outputs(q, k, dq_out, dk_out, False, stream)
     dev = q.device
     with _AllocOn(stream, dev):
-        if dwq_out is None:
-            dwq_out = torch.empty(dq, dtype=torch.float32, device=dev)
-        if has_k and dwk_out is None:
-            dwk_out = torch.empty(dk, dtype=torch.float32, device=dev)
+        dwq_out = _f32_vector(dwq_out, "dwq_out", wq)
+        dwk_out = _f32_vector(dwk_out, "dwk_out", wk) if has_k else None
         if workspace is None:
-            workspace = torch.empty(_rotary_workspace(dev, T, dq, dk), dtype=torch.uint8, device=dev)
-    for name, t, n in (("dwq_out", dwq_out, dq), ("dwk_out", dwk_out if has_k else None, dk)):
-        if t is not None:
-            _vec(t, name, n)
-            if t.dtype != torch.float32:
-                raise ValueError(f"{name} must be fp32")
+            workspace = wq.new_empty(_rotary_workspace(dev, T, dq, dk), dtype=torch.uint8)
     _cuda(workspace, "workspace")
     _call("qknorm_rotary_backward", dev,
           (gq.data_ptr(), gk.data_ptr() if has_k else None, q.data_ptr(), k.data_ptr() if has_k else None,
@@ -847,8 +853,8 @@ def qknorm_rotary_backward(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.T
            eps, workspace.data_ptr(), workspace.numel() * workspace.element_size()), stream,
           (("gq", gq), ("k", k), ("gk", gk), ("wq", wq), ("wk", wk if has_k else None),
            ("positions", positions if inv_freq is not None else None), ("inv_freq", inv_freq), ("dq_out", dq_t),
-           ("dk_out", dk_t), ("dwq_out", dwq_out), ("dwk_out", dwk_out if has_k else None), ("workspace", workspace)))
-    return dq_t, dk_t, dwq_out, (dwk_out if has_k else None)
+           ("dk_out", dk_t), ("dwq_out", dwq_out), ("dwk_out", dwk_out), ("workspace", workspace)))
+    return dq_t, dk_t, dwq_out, dwk_out
 
 
 _ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}

@@ -246,8 +246,11 @@ __global__ void __launch_bounds__(kBlock) dw_reduce_kernel(const float *__restri
     __shared__ float red[8][33];
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
     const int d = dq + dk;
+    // launched as a programmatic dependent: its blocks may start while the partial sums are formed
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float s = 0.f;
     if (col < d)
+#pragma unroll 4
         for (int i = k; i < slices; i += 8) s += part[(int64_t)i * d + col];
     red[k][threadIdx.x & 31] = s;
     __syncthreads();
@@ -274,7 +277,18 @@ constexpr int kScalarSlices = 64;
 
 qkn_status launch_dw_reduce(const Args &a, int slices, cudaStream_t s) {
     const int dq = a.job[0].d, dk = a.njobs > 1 ? a.job[1].d : 0;
-    dw_reduce_kernel<<<(unsigned)((dq + dk + 31) / 32), kBlock, 0, s>>>(a.part, a.job[0].dw, a.job[1].dw, dq, dk, slices);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((dq + dk + 31) / 32), 1, 1);
+    cfg.blockDim = dim3(kBlock, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, dw_reduce_kernel, (const float *)a.part, a.job[0].dw, a.job[1].dw, dq, dk,
+                                             slices);
+    if (e != cudaSuccess) return cuda_fail(e, "dw_reduce_kernel launch");
     return check_launch("dw_reduce_kernel launch");
 }
 
