@@ -23,8 +23,10 @@
 // keeps at positions j and j + r / 2E (filled in the order the layout asks
 // for), so neighbouring threads read neighbouring 16-byte words.  Chunks
 // behind the rotated part form units of their own, copied (or only
-// normalised).  Fixed columns keep the weights' gradients in registers over
-// all tokens; the weights are read from a copy in shared memory.
+// normalised).  Rows so narrow that one warp has lanes to spare go several
+// tokens to a stage, each with its share of the warp's lanes (and its table).
+// Fixed columns keep the weights' gradients in registers over all tokens; the
+// weights are read from a copy in shared memory.
 //
 // With the norm, consumers meet at one barrier per token: before it they read
 // their chunks, add up squares, multiply by the weights and park their warp's
@@ -67,7 +69,8 @@ struct Params {
     float *part;             // gradients: [gridDim.x][dq + dk]
     int warps, groups;       // consumer warps per group, groups per block
     int warps0;              // consumer warps of job 0 (== warps when one warp serves both jobs)
-    int stages, stage_bytes, x_bytes;
+    int stages, stage_bytes, x_bytes;  // x_bytes: the rows of one token
+    int tokens, lanes;       // tokens per stage (a power of two), lanes per token
     int w_bytes, w_bf16;     // the block's fp32 copy of the weights, in front of the rings; their type in memory
     uint64_t wait_ns;
 };
@@ -230,13 +233,26 @@ __device__ __forceinline__ float warp_sum_of_two(float a, float b, int lane) {
     return v;
 }
 
+// The sum over the lanes of a token.
+__device__ __forceinline__ float token_sum(float v, int lanes) {
+    for (int off = lanes >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
 // Threads of a block: 20 warps leave a thread 96 registers, 16 warps 128 (the
 // gradients, and the variant with twice the units).
 template <int MODE, int UPT, int E> constexpr int max_threads() { return MODE == kNormBack || UPT * E > 16 ? 512 : 640; }
 
-// MIXED: warps serve both tensors (with the norm, one warp); otherwise q and k have warps of their own.
-template <typename TA, int MODE, int UPT, bool HALF, bool MIXED>
+// How the warps of a group divide the rows.
+enum Shape {
+    SPLIT,  // q and k have warps of their own
+    MIXED,  // warps serve both tensors (with the norm, one warp does)
+    MULTI   // one warp serves both tensors of several tokens at a time
+};
+
+template <typename TA, int MODE, int UPT, bool HALF, int SHAPE>
 __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rotary_unit_kernel(const Params a) {
+    constexpr bool BOTH = SHAPE != SPLIT, BATCH = SHAPE == MULTI;
     constexpr int E = Chunk<TA>::E, H = E / 2;
     constexpr bool NORM = MODE != kRotate, BACK = MODE == kNormBack;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -244,37 +260,60 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
     const int group = threadIdx.x / gthreads, gt = threadIdx.x - group * gthreads;  // thread within its group
     const int lane = threadIdx.x & 31, gw = gt >> 5;
     uint8_t *rings = smem + a.w_bytes;
-    uint8_t *fix_p = rings + (size_t)a.groups * a.stages * a.stage_bytes + (size_t)group * group_fixed(a.r, a.stages);
+    uint8_t *fix_p = rings + (size_t)a.groups * a.stages * a.stage_bytes + (size_t)group * group_fixed(a.r * a.tokens, a.stages);
     const uint32_t ring = smem_u32(rings + (size_t)group * a.stages * a.stage_bytes);
-    const int tbytes = table_bytes(a.r);
+    const int tbytes = table_bytes(a.r * a.tokens);
     float *red = reinterpret_cast<float *>(fix_p + (size_t)a.stages * tbytes);
     const uint32_t full = smem_u32(red + 8 * kSlots), empty = full + 8u * a.stages;
+    // Tokens are taken `tokens` at a time: batch n holds tokens n * tokens ...
+    const int per = BATCH ? a.tokens : 1;
+    const int64_t batches = BATCH ? (a.T + per - 1) / per : a.T;
     const int64_t step = (int64_t)gridDim.x * a.groups;
-    const int64_t first_token = (int64_t)group * gridDim.x + blockIdx.x;  // few tokens spread over the SMs first
+    const int64_t first_batch = (int64_t)group * gridDim.x + blockIdx.x;  // few tokens spread over the SMs first
+    const int g_off = a.x_bytes * per;  // of the gradients in a stage
 
-    // copies of a token's rows into a stage (one lane)
+    // copies of a batch's rows into a stage (the producer warp)
     auto fill = [&](int64_t n, int stage) {
         const uint32_t bar = full + 8u * stage, dst = ring + (uint32_t)(stage * a.stage_bytes);
-        mbar_arrive_expect_tx(bar, (uint32_t)a.stage_bytes);
-        bulk_g2s(dst, a.job[0].x + n * a.job[0].ldx, a.job[0].row_bytes, bar);
-        if (BACK) bulk_g2s(dst + a.x_bytes, a.job[0].g + n * a.job[0].ldg, a.job[0].row_bytes, bar);
-        if (a.njobs > 1) {
-            bulk_g2s(dst + a.job[1].row_off, a.job[1].x + n * a.job[1].ldx, a.job[1].row_bytes, bar);
-            if (BACK)
-                bulk_g2s(dst + a.x_bytes + a.job[1].row_off, a.job[1].g + n * a.job[1].ldg, a.job[1].row_bytes, bar);
+        if constexpr (!BATCH) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, (uint32_t)a.stage_bytes);
+                bulk_g2s(dst, a.job[0].x + n * a.job[0].ldx, a.job[0].row_bytes, bar);
+                if (BACK) bulk_g2s(dst + a.x_bytes, a.job[0].g + n * a.job[0].ldg, a.job[0].row_bytes, bar);
+                if (a.njobs > 1) {
+                    bulk_g2s(dst + a.job[1].row_off, a.job[1].x + n * a.job[1].ldx, a.job[1].row_bytes, bar);
+                    if (BACK)
+                        bulk_g2s(dst + a.x_bytes + a.job[1].row_off, a.job[1].g + n * a.job[1].ldg, a.job[1].row_bytes, bar);
+                }
+            }
+        } else {
+            const int64_t t0 = n * per;
+            const int rows = a.T - t0 < per ? (int)(a.T - t0) : per;
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(rows * a.x_bytes * (BACK ? 2 : 1)));
+            __syncwarp();
+            for (int i = lane; i < rows * a.njobs; i += 32) {
+                const int t = a.njobs > 1 ? i >> 1 : i;
+                const Rows J = pick(a, a.njobs > 1 ? i & 1 : 0);
+                const uint32_t to = dst + (uint32_t)(t * a.x_bytes + J.row_off);
+                bulk_g2s(to, J.x + (t0 + t) * J.ldx, J.row_bytes, bar);
+                if (BACK) bulk_g2s(to + g_off, J.g + (t0 + t) * J.ldg, J.row_bytes, bar);
+            }
         }
     };
-    uint32_t issued = 0;  // stages filled (the producer's lane 0)
-    if (gw == a.warps && lane == 0) {
-        for (int s = 0; s < a.stages; ++s) {
-            mbar_init(full + 8u * s, 2);         // the producer's two arrivals and the copies' bytes
-            mbar_init(empty + 8u * s, a.warps);  // one per consumer warp
+    uint32_t issued = 0;  // stages filled (the producer warp)
+    if (gw == a.warps) {
+        if (lane == 0) {
+            for (int s = 0; s < a.stages; ++s) {
+                mbar_init(full + 8u * s, 2);         // the producer's two arrivals and the copies' bytes
+                mbar_init(empty + 8u * s, a.warps);  // one per consumer warp
+            }
+            mbar_init_fence();
         }
-        mbar_init_fence();
+        __syncwarp();
         // the previous kernel on the stream has finished before any global memory is touched
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        int64_t n = first_token;
-        for (int s = 0; s < a.stages && n < a.T; ++s, n += step) {
+        int64_t n = first_batch;
+        for (int s = 0; s < a.stages && n < batches; ++s, n += step) {
             fill(n, s);
             issued |= 1u << s;
         }
@@ -326,21 +365,35 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
         int stage = 0;
         uint32_t phase = 0;
         bool first = true;  // the first round of stages is filled already
-        int64_t p = pos_at(first_token);
-        for (int64_t n = first_token; n < a.T; n += step) {
+        int64_t p = pos_at(first_batch * per + (BATCH ? lane % per : 0));  // lane t holds token t's position
+        for (int64_t n = first_batch; n < batches; n += step) {
             const uint32_t bar = full + 8u * stage;
             if (!first) {
                 const bool ok = mbar_wait_fast(empty + 8u * stage, phase ^ 1u, &g_rotary_error, a.wait_ns);
                 if (__any_sync(0xffffffffu, !ok)) break;
-                if (lane == 0) fill(n, stage);
+                fill(n, stage);
             }
-            const int64_t next = pos_at(n + step);
+            const int64_t next = pos_at((n + step) * per + (BATCH ? lane % per : 0));
             float *t = reinterpret_cast<float *>(fix_p + (size_t)stage * tbytes);
+            // one token after the other where its pairs fill the warp, all at once where they do not
+            if (BATCH && nf < 32) {
+                for (int i0 = 0; i0 < per * nf; i0 += 32) {
+                    const int i = i0 + lane, tok = min(i / nf, per - 1), f = i - i / nf * nf;
+                    const int64_t pt = __shfl_sync(0xffffffffu, p, tok);
+                    float *tt = t + tok * a.r;
+                    if (i < per * nf)
+                        cos_sin(pt, __ldg(a.freq + f) * kInvTwoPi, a.mscale, a.sign, tt[place(f)], tt[nf + place(f)]);
+                }
+            } else {
+                for (int tok = 0; tok < per; ++tok, t += a.r) {
+                    const int64_t pt = BATCH ? __shfl_sync(0xffffffffu, p, tok) : p;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (lane + 32 * i < nf) cos_sin(p, turns[i], a.mscale, a.sign, t[at[i]], t[nf + at[i]]);
-            for (int f = lane + 64; f < nf; f += 32)
-                cos_sin(p, __ldg(a.freq + f) * kInvTwoPi, a.mscale, a.sign, t[place(f)], t[nf + place(f)]);
+                    for (int i = 0; i < 2; ++i)
+                        if (lane + 32 * i < nf) cos_sin(pt, turns[i], a.mscale, a.sign, t[at[i]], t[nf + at[i]]);
+                    for (int f = lane + 64; f < nf; f += 32)
+                        cos_sin(pt, __ldg(a.freq + f) * kInvTwoPi, a.mscale, a.sign, t[place(f)], t[nf + place(f)]);
+                }
+            }
             p = next;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
@@ -360,13 +413,13 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- consumer warps
-        const bool wk = !MIXED && gw >= a.warps0;  // a warp of the keys
+        const bool wk = !BOTH && gw >= a.warps0;  // a warp of the keys
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
             int which = wk ? 1 : 0;
             const int jw = wk ? a.warps - a.warps0 : a.warps0;
-            int u = gt - (wk ? a.warps0 * 32 : 0) + i * jw * 32;
-            if (MIXED && u >= a.job[0].nunits) {
+            int u = BATCH ? lane % a.lanes + i * a.lanes : gt - (wk ? a.warps0 * 32 : 0) + i * jw * 32;
+            if (BOTH && u >= a.job[0].nunits) {
                 u -= a.job[0].nunits;
                 which = 1;
             }
@@ -405,27 +458,30 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
         if (!BACK) same = __all_sync(0xffffffffu, same);
         const float d_q = (float)a.job[0].d, d_k = (float)a.job[1].d;
         // rows of the results, moved by the chunk's place in a stage
-        uint8_t *yq = (wk ? a.job[1].y - a.job[1].row_off : a.job[0].y) + first_token * (wk ? a.job[1].ldy : a.job[0].ldy);
-        uint8_t *yk = MIXED ? a.job[1].y - a.job[1].row_off + first_token * a.job[1].ldy : nullptr;
-        const int64_t yq_step = step * (wk ? a.job[1].ldy : a.job[0].ldy), yk_step = step * a.job[1].ldy;
+        const int sub = BATCH ? lane / a.lanes : 0;  // this lane's token of a batch
+        int64_t token = first_batch * per + sub;
+        uint8_t *yq = (wk ? a.job[1].y - a.job[1].row_off : a.job[0].y) + token * (wk ? a.job[1].ldy : a.job[0].ldy);
+        uint8_t *yk = BOTH ? a.job[1].y - a.job[1].row_off + token * a.job[1].ldy : nullptr;
+        const int64_t yq_step = step * per * (wk ? a.job[1].ldy : a.job[0].ldy), yk_step = step * per * a.job[1].ldy;
         const int my_warps = wk ? a.warps - a.warps0 : a.warps0, my_warp = wk ? gw - a.warps0 : gw;
 
         int stage = 0, par = 0;
         uint32_t phase = 0;
-        // tokens of this group (fewer than 2^31)
-        for (int left = first_token < a.T ? (int)((a.T - first_token - 1) / step) + 1 : 0; left > 0; --left) {
+        // batches of this group (fewer than 2^31)
+        for (int left = first_batch < batches ? (int)((batches - first_batch - 1) / step) + 1 : 0; left > 0; --left) {
             const bool ok = mbar_wait_fast(full + 8u * stage, phase, &g_rotary_error, a.wait_ns);
-            const uint32_t src = ring + (uint32_t)(stage * a.stage_bytes);
-            const uint32_t tab_s = tables + (uint32_t)(stage * tbytes);
+            const uint32_t src = ring + (uint32_t)(stage * a.stage_bytes + (BATCH ? sub * a.x_bytes : 0));
+            const uint32_t tab_s = tables + (uint32_t)(stage * tbytes + (BATCH ? sub * a.r * 4 : 0));
+            const bool live = !BATCH || token < a.T;  // the last batch may have fewer tokens
             float2 va[UPT][H], vb[UPT][H];  // rotary: x; with the norm: x w; gradients: g, dy turned back
             float2 sq[2] = {both(0.f), both(0.f)}, pg[2] = {both(0.f), both(0.f)};  // sums of x^2 and of w g x
             Turns<H> cs;
-
 #pragma unroll
             for (int i = 0; i < UPT; ++i) {
-                const uint32_t pa = off_a[i] >= 0 ? src + off_a[i] : zeros, pb = off_b[i] >= 0 ? src + off_b[i] : zeros;
+                const bool has_a = live && off_a[i] >= 0, has_b = live && off_b[i] >= 0;
+                const uint32_t pa = has_a ? src + off_a[i] : zeros, pb = has_b ? src + off_b[i] : zeros;
                 const uint32_t qa = w_s + max(off_a[i], 0), qb = w_s + max(off_b[i], 0);
-                const int m = MIXED ? (is_k >> i) & 1u : 0;
+                const int m = BOTH ? (is_k >> i) & 1u : 0;
                 if constexpr (MODE == kRotate) {
                     unpack2<TA, H>(lds128(pa), va[i]);
                     unpack2<TA, H>(lds128(pb), vb[i]);
@@ -446,8 +502,8 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
                     if (m) sq[1] = __fadd2_rn(sq[1], q);
                     else sq[0] = __fadd2_rn(sq[0], q);
                 } else {
-                    unpack2<TA, H>(lds128(off_a[i] >= 0 ? pa + a.x_bytes : zeros), va[i]);
-                    unpack2<TA, H>(lds128(off_b[i] >= 0 ? pb + a.x_bytes : zeros), vb[i]);
+                    unpack2<TA, H>(lds128(has_a ? pa + g_off : zeros), va[i]);
+                    unpack2<TA, H>(lds128(has_b ? pb + g_off : zeros), vb[i]);
                     if (tab[i] >= 0) {
                         cs.load(tab_s + tab[i], run, sin_off);
                         turn<H, HALF, false>(va[i], vb[i], cs, 1.f);
@@ -480,11 +536,12 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
             bool failed = !ok;
             if constexpr (NORM) {
                 float s, t = 0.f;
-                if constexpr (MIXED) {
-                    s = warp_sum(sq[0].x + sq[0].y);
-                    if (BACK) t = warp_sum(pg[0].x + pg[0].y);
-                    inv_k = rsqrtf(warp_sum(sq[1].x + sq[1].y) / d_k + a.eps);
-                    if (BACK) ck = inv_k * inv_k * (warp_sum(pg[1].x + pg[1].y) / d_k);
+                if constexpr (BOTH) {
+                    const int lanes = BATCH ? a.lanes : 32;
+                    s = token_sum(sq[0].x + sq[0].y, lanes);
+                    if (BACK) t = token_sum(pg[0].x + pg[0].y, lanes);
+                    inv_k = rsqrtf(token_sum(sq[1].x + sq[1].y, lanes) / d_k + a.eps);
+                    if (BACK) ck = inv_k * inv_k * (token_sum(pg[1].x + pg[1].y, lanes) / d_k);
                     failed = __any_sync(0xffffffffu, failed);
                 } else {
                     // the sums of this token: [q | k][x^2 | w g x][kSlots], slots without a warp hold zero
@@ -511,6 +568,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
                 const float d = wk ? d_k : d_q;
                 inv_q = rsqrtf(s / d + a.eps);
                 if (BACK) cq = inv_q * inv_q * (t / d);
+                if (BATCH && !live) inv_q = inv_k = cq = ck = 0.f;  // no row: nothing for the weights' sums
             } else {
                 failed = __any_sync(0xffffffffu, failed);
             }
@@ -518,28 +576,29 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
             if (!BACK && same && tab[0] >= 0) cs.load(tab_s + tab[0], run, sin_off);
 #pragma unroll
             for (int i = 0; i < UPT; ++i) {
-                const bool m = MIXED && ((is_k >> i) & 1u);
+                const bool has_a = live && off_a[i] >= 0, has_b = live && off_b[i] >= 0;
+                const bool m = BOTH && ((is_k >> i) & 1u);
                 const float inv = m ? inv_k : inv_q;
                 uint8_t *y = m ? yk : yq;
                 if constexpr (BACK) {
                     const float2 nc = both(-(m ? ck : cq)), inv2 = both(inv);
                     float2 w[H], x[H];
-                    unpack2<TA, H>(lds128(off_a[i] >= 0 ? src + off_a[i] : zeros), x);
+                    unpack2<TA, H>(lds128(has_a ? src + off_a[i] : zeros), x);
                     lds_weights<H>(w_s + max(off_a[i], 0), upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) {
                         da[i][p] = __ffma2_rn(va[i][p], __fmul2_rn(x[p], inv2), da[i][p]);
                         va[i][p] = __fmul2_rn(inv2, __ffma2_rn(x[p], nc, __fmul2_rn(w[p], va[i][p])));
                     }
-                    if (off_a[i] >= 0) st_stream_batched(y + off_a[i], pack2<TA, H>(va[i]));
-                    unpack2<TA, H>(lds128(off_b[i] >= 0 ? src + off_b[i] : zeros), x);
+                    if (has_a) st_stream_batched(y + off_a[i], pack2<TA, H>(va[i]));
+                    unpack2<TA, H>(lds128(has_b ? src + off_b[i] : zeros), x);
                     lds_weights<H>(w_s + max(off_b[i], 0), upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) {
                         db[i][p] = __ffma2_rn(vb[i][p], __fmul2_rn(x[p], inv2), db[i][p]);
                         vb[i][p] = __fmul2_rn(inv2, __ffma2_rn(x[p], nc, __fmul2_rn(w[p], vb[i][p])));
                     }
-                    if (off_b[i] >= 0) st_stream_batched(y + off_b[i], pack2<TA, H>(vb[i]));
+                    if (has_b) st_stream_batched(y + off_b[i], pack2<TA, H>(vb[i]));
                 } else {
                     if (tab[i] >= 0) {
                         if (!same) cs.load(tab_s + tab[i], run, sin_off);
@@ -551,12 +610,13 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
                             vb[i][p] = __fmul2_rn(vb[i][p], both(inv));
                         }
                     }
-                    if (off_a[i] >= 0) st_stream_batched(y + off_a[i], pack2<TA, H>(va[i]));
-                    if (off_b[i] >= 0) st_stream_batched(y + off_b[i], pack2<TA, H>(vb[i]));
+                    if (has_a) st_stream_batched(y + off_a[i], pack2<TA, H>(va[i]));
+                    if (has_b) st_stream_batched(y + off_b[i], pack2<TA, H>(vb[i]));
                 }
             }
             yq += yq_step;
-            if (MIXED) yk += yk_step;
+            if (BOTH) yk += yk_step;
+            if (BATCH) token += step * per;
             __syncwarp();  // the warp has read the stage and its table
             if (lane == 0) mbar_arrive(empty + 8u * stage);
             if (++stage == a.stages) {
@@ -573,7 +633,18 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
         float *out = a.part + (int64_t)blockIdx.x * d;
         float *mine = a.groups > 1 ? reinterpret_cast<float *>(rings) + (size_t)group * d : out;
         __syncthreads();  // every group has read its last stage
-        if (gw < a.warps) {
+        if (BATCH && gw < a.warps)  // the sums of a batch's tokens meet in the lanes of the first
+            for (int off = a.lanes; off < 32; off <<= 1)
+#pragma unroll
+                for (int i = 0; i < UPT; ++i)
+#pragma unroll
+                    for (int p = 0; p < H; ++p) {
+                        da[i][p].x += __shfl_xor_sync(0xffffffffu, da[i][p].x, off);
+                        da[i][p].y += __shfl_xor_sync(0xffffffffu, da[i][p].y, off);
+                        db[i][p].x += __shfl_xor_sync(0xffffffffu, db[i][p].x, off);
+                        db[i][p].y += __shfl_xor_sync(0xffffffffu, db[i][p].y, off);
+                    }
+        if (gw < a.warps && (!BATCH || lane < a.lanes)) {
 #pragma unroll
             for (int i = 0; i < UPT; ++i) {
                 if (off_a[i] < 0) continue;
@@ -605,8 +676,9 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
 
 struct Plan {
     bool fits;
-    int upt, warps, warps0, groups, threads;
+    int upt, warps, warps0, groups, threads, tokens;
     bool mixed;
+
 };
 
 // Whether the unit kernel takes the call, and its geometry: a rule on the
@@ -655,13 +727,17 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
     constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
     const int most = MODE == kNormBack ? kUsual : 4;
     r.upt = kUsual;
-    r.mixed = MODE == kRotate || (a.njobs > 1 && u0 + u1 <= 32 * kUsual);
+    r.mixed = MODE == kRotate || u0 + u1 <= 32 * kUsual;
     for (;; r.upt *= 2) {
         if (r.upt > most) return r;
         r.warps0 = r.mixed ? warps_of(u0 + u1, r.upt) : warps_of(u0, r.upt);
         r.warps = r.mixed ? r.warps0 : r.warps0 + warps_of(u1, r.upt);
         if (r.warps <= kMaxWarps) break;
     }
+    // several tokens to a stage while one warp has the lanes for them
+    r.tokens = 1;
+    while (r.mixed && r.warps == 1 && r.tokens < 8 && (u0 + u1) * r.tokens * 2 <= 32 * r.upt) r.tokens *= 2;
+    p.stage_bytes *= r.tokens;
     // groups side by side in a block (one block per SM, so that they share the weights' copy)
     r.groups = (MODE == kNormBack || r.upt * E > 16 ? 16 : 20) / (r.warps + 1);
     r.threads = r.groups * (r.warps + 1) * 32;
@@ -669,9 +745,9 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
     return r;
 }
 
-template <typename TA, int MODE, int UPT, bool HALF, bool MIXED>
+template <typename TA, int MODE, int UPT, bool HALF, int SHAPE>
 qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bool *taken) {
-    const auto kernel = rotary_unit_kernel<TA, MODE, UPT, HALF, MIXED>;
+    const auto kernel = rotary_unit_kernel<TA, MODE, UPT, HALF, SHAPE>;
     static std::atomic<bool> attr_set[64];
     int dev = 0;
     cudaGetDevice(&dev);
@@ -683,12 +759,13 @@ qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bo
     }
     int smem = 0;
     for (p.stages = 8; p.stages >= 1; --p.stages) {
-        smem = p.w_bytes + p.groups * (p.stages * p.stage_bytes + group_fixed(p.r, p.stages));
+        smem = p.w_bytes + p.groups * (p.stages * p.stage_bytes + group_fixed(p.r * p.tokens, p.stages));
         if (smem <= kSmemLimit) break;
     }
     *taken = p.stages >= 1;
     if (!*taken) return QKN_OK;
-    *grid = (int)(p.T < sm_count() ? p.T : sm_count());
+    const int64_t batches = (p.T + p.tokens - 1) / p.tokens;
+    *grid = (int)(batches < sm_count() ? batches : sm_count());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)*grid, 1, 1);
     cfg.blockDim = dim3((unsigned)r.threads, 1, 1);
@@ -704,10 +781,10 @@ qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bo
     return check_launch("rotary_unit_kernel launch");
 }
 
-template <typename TA, int MODE, int UPT, bool MIXED>
+template <typename TA, int MODE, int UPT, int SHAPE>
 qkn_status launch_layout(Params &p, const Plan &r, int layout, int *grid, cudaStream_t s, bool *taken) {
-    return layout == QKN_ROTARY_HALF ? launch_kernel<TA, MODE, UPT, true, MIXED>(p, r, grid, s, taken)
-                                     : launch_kernel<TA, MODE, UPT, false, MIXED>(p, r, grid, s, taken);
+    return layout == QKN_ROTARY_HALF ? launch_kernel<TA, MODE, UPT, true, SHAPE>(p, r, grid, s, taken)
+                                     : launch_kernel<TA, MODE, UPT, false, SHAPE>(p, r, grid, s, taken);
 }
 
 // Launches the unit kernel when it takes the call (*taken); *grid is its number of blocks.
@@ -730,17 +807,20 @@ qkn_status launch(const Args &a, bool *taken, int *grid, cudaStream_t s) {
     p.warps = r.warps;
     p.warps0 = r.warps0;
     p.groups = r.groups;
+    p.tokens = r.tokens;
+    p.lanes = 32 / r.tokens;
     p.wait_ns = kWaitTimeoutNs;
     p.w_bf16 = sizeof(TW) == 2;
     p.w_bytes = (MODE == kRotate ? 0 : (p.job[0].d + p.job[1].d) * 4) + 16;  // 16 bytes of zeros
     constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
+    if (r.tokens > 1) return launch_layout<TA, MODE, kUsual, MULTI>(p, r, a.layout, grid, s, taken);
     if constexpr (MODE == kRotate) {
-        if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, true>(p, r, a.layout, grid, s, taken);
-        if constexpr (kUsual < 4) return launch_layout<TA, MODE, 4, true>(p, r, a.layout, grid, s, taken);
+        if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, MIXED>(p, r, a.layout, grid, s, taken);
+        if constexpr (kUsual < 4) return launch_layout<TA, MODE, 4, MIXED>(p, r, a.layout, grid, s, taken);
     } else {
-        if (r.mixed) return launch_layout<TA, MODE, kUsual, true>(p, r, a.layout, grid, s, taken);
-        if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, false>(p, r, a.layout, grid, s, taken);
-        if constexpr (MODE == kNorm && kUsual < 4) return launch_layout<TA, MODE, 4, false>(p, r, a.layout, grid, s, taken);
+        if (r.mixed) return launch_layout<TA, MODE, kUsual, MIXED>(p, r, a.layout, grid, s, taken);
+        if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, SPLIT>(p, r, a.layout, grid, s, taken);
+        if constexpr (MODE == kNorm && kUsual < 4) return launch_layout<TA, MODE, 4, SPLIT>(p, r, a.layout, grid, s, taken);
     }
     return fail(QKN_ERR_UNSUPPORTED, "rotary_unit_kernel: no variant for these rows");
 }

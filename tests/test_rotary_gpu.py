@@ -292,6 +292,30 @@ def test_zero_rows_and_zero_tokens(cuda_lib):
     assert got[0].shape == (0, 128) and bool((dw == 0).all()) and bool((got[3] == 0).all())
 
 
+@pytest.mark.parametrize("T", [1, 5, 8, 13, 2500])
+def test_narrow_rows_share_a_warp(cuda_lib, T):
+    # rows of a few chunks go several tokens to a warp; the last ones may be missing, and with
+    # eps = 0 nothing of the places without a token may reach the weights' gradients
+    for hq, hk, D, r, dtype in ((1, 1, 16, 16, torch.bfloat16), (1, 1, 64, 64, torch.bfloat16), (2, 1, 64, 32, torch.float32),
+                                (1, 1, 128, 128, torch.bfloat16), (1, 0, 64, 64, torch.float32)):
+        s = make(T, hq, hk, D, r, dtype, seed=T)
+        d = dev(s)
+        args = (d["q"], d["k"], d["wq"], d["wk"], d["pos"], d["freq"], D, 0.0)
+        fwd = qk.qknorm_rotary(*args)
+        got = qk.qknorm_rotary_backward(d["gq"], d["gk"], *args)
+        for n, o, dx, dw in (("q", fwd[0], got[0], got[2]), ("k", fwd[1], got[1], got[3])):
+            if o is None:
+                continue
+            y, e = norm(f64(s[n]), f64(s["w" + n]), 0.0)
+            ref, err = rotate(y, e, s["pos"].numpy(), freqs(s), 1.0, D, "half", 1)
+            close(o, ref, err, dtype, n)
+            g = f64(s["g" + n])
+            g, ge = rotate(g, np.zeros_like(g), s["pos"].numpy(), freqs(s), 1.0, D, "half", -1)
+            ref, err, dwr, dwe = norm_back(f64(s[n]), f64(s["w" + n]), g, ge, 0.0)
+            close(dx, ref, err, dtype, "d" + n)
+            close(dw, dwr, dwe, torch.float32, "dw" + n)
+
+
 def test_norm_without_rotation_is_qknorm(cuda_lib):
     # the same statistic in another order of summation: bf16 results at most one step apart
     s = make(300, 8, 4, 128, 0, torch.bfloat16, seed=31)
