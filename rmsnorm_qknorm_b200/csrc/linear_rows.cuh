@@ -27,7 +27,7 @@ constexpr int BK = 64;
 constexpr int THREADS = 192;
 constexpr int W_BYTES = BF * BK * 2;       // 16 KiB
 constexpr int kMaxCluster = 8;
-constexpr int kMinBlocks = 4;              // k blocks per CTA at least, where K is split
+constexpr int kMinBlocks = 4;              // blocks of k per CTA at least, where K is split
 template <int BT> constexpr int stage_bytes() { return W_BYTES + BT * BK * 2; }
 // two CTAs per SM: at most 113 KiB each
 template <int BT> constexpr int stages() { return (112 * 1024 - 2048) / stage_bytes<BT>(); }
@@ -236,6 +236,18 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
 
 // ---------------------------------------------------------------- host side
 
+// CTAs that share a tile's K: up to one CTA per SM over kMinBlocks blocks of k each, or up to two,
+// less an eighth that clusters cannot use, over four times as many.  One token: 12288 x 4096 21.6 us
+// over 192 CTAs, 24.9 over 96 and 29.9 over 288, more than run at once; 4096 x 12288 18.9 split in
+// 8, 19.6 in 4; 4096 x 4096 9.1 split in 8, 8.8 in 4.
+inline int64_t split_of(int64_t tiles, int64_t k_blocks) {
+    const int64_t sms = sm_count();
+    const int64_t one = std::min<int64_t>(k_blocks / kMinBlocks, sms / tiles);
+    const int64_t two = std::min<int64_t>(k_blocks / (4 * kMinBlocks), 7 * sms / 4 / tiles);
+    const int64_t s = std::min<int64_t>(kMaxCluster, std::max(one, two));
+    return s < 1 ? 1 : s;
+}
+
 template <int BT, int ACT>
 qkn_status launch_bt(const pair::Matrix &x, const pair::Matrix &W, const Args &a, cudaStream_t s) {
     const auto kernel = linear_rows_kernel<BT, ACT>;
@@ -263,26 +275,7 @@ qkn_status launch_bt(const pair::Matrix &x, const pair::Matrix &W, const Args &a
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    // K is split over as many CTAs as leave every cluster resident at once (a second wave costs
-    // more than the wider split gains: one token, 12288 x 4096, 21.6 us over 192 CTAs, 29.9 us
-    // over 288 that do not all fit), each over at least kMinBlocks blocks of k
-    static std::atomic<int> resident[64][kMaxCluster + 1];  // per device and cluster size; 0 until asked
-    int64_t split = kMaxCluster;
-    if (split > a.k_blocks / kMinBlocks) split = a.k_blocks / kMinBlocks;
-    for (; split > 1; --split) {
-        int n = known ? resident[dev][split].load(std::memory_order_relaxed) : 0;
-        if (n == 0) {
-            attr[0].val.clusterDim.x = (unsigned)split;
-            cfg.gridDim = dim3((unsigned)split, 1, 1);
-            cfg.numAttrs = 1;
-            const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-            if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(linear_rows_kernel)");
-            if (n < 1) n = 1;
-            if (known) resident[dev][split].store(n, std::memory_order_relaxed);
-        }
-        if (tiles * token_tiles <= n) break;
-    }
-    if (split < 1) split = 1;
+    const int64_t split = split_of(tiles * token_tiles, a.k_blocks);
     cfg.numAttrs = 2;
     cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)token_tiles, 1);
     attr[0].val.clusterDim.x = (unsigned)split;
@@ -298,8 +291,7 @@ qkn_status launch_bt(const pair::Matrix &x, const pair::Matrix &W, const Args &a
 inline int64_t cost(int64_t M, int64_t N, int64_t K, int bt) {
     const int64_t sms = sm_count(), kb = (K + BK - 1) / BK, tiles = ((N + BF - 1) / BF) * ((M + bt - 1) / bt);
     const int64_t c = bt == 16 ? 190 : bt == 32 ? 200 : bt == 64 ? 300 : 480;
-    int64_t split = std::min<int64_t>(std::min<int64_t>(kMaxCluster, kb / kMinBlocks), 7 * sms / 4 / tiles);
-    if (split < 1) split = 1;
+    const int64_t split = split_of(tiles, kb);
     return 3500 + (tiles * split + sms - 1) / sms * ((kb + split - 1) / split * c + 25 * std::min<int64_t>(bt, M) / split);
 }
 
