@@ -136,8 +136,8 @@ qkn_status launch_dz(const __nv_bfloat16 *dy, const __nv_bfloat16 *z, __nv_bfloa
 template <int ACT>
 qkn_status forward(const pair::Matrix &x, const pair::Matrix &W, const pair::Matrix &y, const pair::Matrix *res,
                    const pair::Matrix *z, const Epilogue &epi, int64_t K, cudaStream_t s) {
-    if (const int tokens = rows::tokens_per_tile(y.rows, y.inner, K))
-        return rows::launch<ACT>(x, W, y, res, z, epi, K, tokens, s);
+    if (const int tokens = rows::tokens_per_tile(y.rows, y.inner, K, true, ACT == QKN_ACT_NONE && !res && !z, 16))
+        return rows::launch<ACT, false, false>(x, W, y, res, z, epi, K, tokens, s);
     return pair::launch<false, false, ACT>(x, W, y, res, z, epi, K, s);
 }
 
@@ -279,11 +279,15 @@ extern "C" QKN_API qkn_status linear_fused_backward(const void *dy, const void *
     const lin::Epilogue e{};
     if (st == QKN_OK && dx != nullptr) {
         const lin::pair::Matrix out = {dx, M, K, lddx};
-        st = lin::pair::launch<false, true, QKN_ACT_NONE>(mg, mw, out, nullptr, nullptr, e, N, s);
+        const int tokens = lin::rows::tokens_per_tile(M, K, N, false, true, 16);
+        st = tokens ? lin::rows::launch<QKN_ACT_NONE, true, false>(mg, mw, out, nullptr, nullptr, e, N, tokens, s)
+                    : lin::pair::launch<false, true, QKN_ACT_NONE>(mg, mw, out, nullptr, nullptr, e, N, s);
     }
     if (st == QKN_OK && dW != nullptr) {
         const lin::pair::Matrix out = {dW, N, K, lddw};
-        st = lin::pair::launch<true, true, QKN_ACT_NONE>(mg, mx, out, nullptr, nullptr, e, M, s);
+        const int tokens = lin::rows::tokens_per_tile(N, K, M, false, true, 64);
+        st = tokens ? lin::rows::launch<QKN_ACT_NONE, true, true>(mg, mx, out, nullptr, nullptr, e, M, tokens, s)
+                    : lin::pair::launch<true, true, QKN_ACT_NONE>(mg, mx, out, nullptr, nullptr, e, M, s);
     }
     if (own != nullptr) {
         const cudaError_t f = cudaFreeAsync(own, s);

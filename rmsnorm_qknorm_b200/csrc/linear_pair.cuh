@@ -436,14 +436,16 @@ qkn_status launch_bn(const Matrix &a, const Matrix &b, const Matrix &y, const Ma
 }
 
 // About how long the kernel takes, in ns: 4 us, and for every round of tiles over the pairs its
-// products (64 k: 340 ns at 256 columns, 240 ns at 128) or, for short K, its epilogue.  Measured
-// with 512 .. 12288 columns, K 512 .. 12288 and 128 .. 2048 rows, gelu and a residual: within a
-// tenth of it, e.g. 512 x 4096 x 4096 27.6 us (256 columns, 32 of 74 pairs) against 20.7 (128),
-// 2048 x 4096 x 4096 52.8 against 70.2.
-inline int64_t cost(int64_t M, int64_t N, int64_t K, int bn) {
+// products (64 k: 340 ns at 256 columns, 240 ns at 128) or, for short K, its epilogue, which an
+// activation, a residual or a kept z makes longer (`plain` without them).  Measured with 512 ..
+// 12288 columns, K 512 .. 12288 and 128 .. 2048 rows, gelu and a residual: within a tenth of it,
+// e.g. 512 x 4096 x 4096 27.6 us (256 columns, 32 of 74 pairs) against 20.7 (128), 2048 x 4096 x
+// 4096 52.8 against 70.2; without them 4096 x 4096 x 64 15.6.
+inline int64_t cost(int64_t M, int64_t N, int64_t K, int bn, bool plain) {
     const int64_t pairs = sm_count() > 1 ? sm_count() / 2 : 1, kb = (K + BK - 1) / BK;
     const int64_t tiles = ((M + 2 * BM - 1) / (2 * BM)) * ((N + bn - 1) / bn);
-    const int64_t round = bn == 256 ? std::max<int64_t>(7000, 2500 + 340 * kb) : std::max<int64_t>(4400, 1500 + 240 * kb);
+    const int64_t round = bn == 256 ? std::max<int64_t>(plain ? 3000 : 7000, 2500 + 340 * kb)
+                                    : std::max<int64_t>(plain ? 2000 : 4400, 1500 + 240 * kb);
     return 4000 + (tiles + pairs - 1) / pairs * round;
 }
 
@@ -458,7 +460,8 @@ qkn_status launch(const Matrix &a, const Matrix &b, const Matrix &y, const Matri
     g.wide = aligned(g.z, 32) && g.ldz % 16 == 0;
     g.M = (int)y.rows;
     g.N = (int)y.inner;
-    const bool narrow = cost(g.M, g.N, K, 128) < cost(g.M, g.N, K, 256);
+    const bool plain = ACT == QKN_ACT_NONE && res == nullptr && z == nullptr;
+    const bool narrow = cost(g.M, g.N, K, 128, plain) < cost(g.M, g.N, K, 256, plain);
     return narrow ? launch_bn<A_MN, B_MN, 128, ACT>(a, b, y, res, g, K, s) : launch_bn<A_MN, B_MN, 256, ACT>(a, b, y, res, g, K, s);
 }
 

@@ -14,6 +14,11 @@
 // CTAs, which add the S partials in rank order over distributed shared memory
 // and run the epilogue.  No workspace, no atomics: the same bits every time.
 //
+// The gradients' products take the same shape where tiles are few and K is
+// long: dx = dz W has W's columns as features, dW = dz^T x the columns of x,
+// with dz's as tokens.  An operand whose features (or tokens) are contiguous in
+// memory is MN-major, as in linear_pair.cuh.
+//
 // Roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 take
 // the accumulator out of tensor memory; all six add up and store.
 // Every wait is bounded and records a failure in g_linear_error.
@@ -41,9 +46,21 @@ struct Args {
     int M, N, k_blocks;
 };
 
-// bf16 A and B, both K-major, fp32 D, M = 128, N = BT
-template <int BT> constexpr uint32_t instr_desc() {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BT >> 3) << 17) | ((uint32_t)(BF >> 4) << 24);
+// bf16 A and B, fp32 D, M = 128, N = BT; bits 15 and 16 mark MN-major operands.
+template <int BT, bool F_MN, bool T_MN> constexpr uint32_t instr_desc() {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((F_MN ? 1u : 0u) << 15) | ((T_MN ? 1u : 0u) << 16) |
+           ((uint32_t)(BT >> 3) << 17) | ((uint32_t)(BF >> 4) << 24);
+}
+
+// ROWS rows x 64 k of an operand into a stage.
+template <bool MN, int ROWS>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int row, int k, uint32_t bar) {
+    if constexpr (MN) {
+#pragma unroll
+        for (int h = 0; h < ROWS / 64; ++h) elect_tma_load(dst + h * 8192u, map, row + 64 * h, k, bar);
+    } else {
+        elect_tma_load(dst, map, k, row, bar);
+    }
 }
 
 __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
@@ -119,11 +136,13 @@ __device__ __forceinline__ void finish(const Args &g, uint32_t tile, const float
     }
 }
 
-template <int BT, int ACT>
+// F_MN, T_MN: the operand of features, of tokens, is MN-major (tokens: 64 or 128 per tile).
+template <int BT, int ACT, bool F_MN, bool T_MN>
 __global__ void __launch_bounds__(THREADS, 2)
 linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x, const Args g) {
     constexpr int STAGES = stages<BT>(), STAGE_BYTES = stage_bytes<BT>();
     constexpr int TMEM_COLS = BT < 32 ? 32 : BT;
+    static_assert(!T_MN || BT % 64 == 0, "an MN-major operand comes in blocks of 64");
     static_assert(BT * BF * 4 <= STAGES * STAGE_BYTES, "the partial tile reuses the ring");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -167,8 +186,8 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
             if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, &g_linear_error)) break;
             const uint32_t fb = smem_u32(&full[stage]), sa = smem_u32(smem + stage * STAGE_BYTES);
             elect_expect_tx(fb, STAGE_BYTES);
-            elect_tma_load(sa, &tmap_w, at * BK, n0, fb);
-            elect_tma_load(sa + W_BYTES, &tmap_x, at * BK, t0, fb);
+            load_operand<F_MN, BF>(sa, &tmap_w, n0, at * BK, fb);
+            load_operand<T_MN, BT>(sa + W_BYTES, &tmap_x, t0, at * BK, fb);
             if (++at == kb1) at = kb0;
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -180,17 +199,17 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
-        const uint64_t a0 = gemm::sw128_kmajor_desc(smem_u32(smem));
+        const uint64_t a0 = pair::operand_desc<F_MN>(smem_u32(smem)), b0 = pair::operand_desc<T_MN>(smem_u32(smem + W_BYTES));
         int stage = 0;
         uint32_t phase = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
             if (!warp_wait(smem_u32(&full[stage]), phase, &g_linear_error)) break;
             gemm::tc_fence_after();
-            const uint64_t ad = a0 + (uint64_t)((stage * STAGE_BYTES) >> 4), bd = ad + (uint64_t)(W_BYTES >> 4);
+            const uint64_t at = (uint64_t)((stage * STAGE_BYTES) >> 4);
 #pragma unroll
             for (int k = 0; k < BK / gemm::UMMA_K; ++k)
-                elect_umma<1, instr_desc<BT>()>(tmem_base, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k),
-                                                (kb != kb0 || k != 0) ? 1u : 0u);
+                elect_umma<1, instr_desc<BT, F_MN, T_MN>()>(tmem_base, a0 + at + k * pair::k_step<F_MN>(),
+                                                            b0 + at + k * pair::k_step<T_MN>(), (kb != kb0 || k != 0) ? 1u : 0u);
             elect_commit<1>(smem_u32(&empty[stage]));
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -248,12 +267,12 @@ inline int64_t split_of(int64_t tiles, int64_t k_blocks) {
     return s < 1 ? 1 : s;
 }
 
-template <int BT, int ACT>
+template <int BT, int ACT, bool F_MN, bool T_MN>
 qkn_status launch_bt(const pair::Matrix &x, const pair::Matrix &W, const Args &a, cudaStream_t s) {
-    const auto kernel = linear_rows_kernel<BT, ACT>;
+    const auto kernel = linear_rows_kernel<BT, ACT, F_MN, T_MN>;
     CUtensorMap tw, tx;
-    if (qkn_status st = make_tmap_pitched(&tw, W.p, W.rows, W.inner, W.pitch, BK, BF, 128)) return st;
-    if (qkn_status st = make_tmap_pitched(&tx, x.p, x.rows, x.inner, x.pitch, BK, BT, 128)) return st;
+    if (qkn_status st = make_tmap_pitched(&tw, W.p, W.rows, W.inner, W.pitch, BK, F_MN ? BK : BF, 128)) return st;
+    if (qkn_status st = make_tmap_pitched(&tx, x.p, x.rows, x.inner, x.pitch, BK, T_MN ? BK : BT, 128)) return st;
     static std::atomic<bool> attr_set[64];  // per device: the attribute has been set
     int dev = 0;
     cudaGetDevice(&dev);
@@ -295,21 +314,23 @@ inline int64_t cost(int64_t M, int64_t N, int64_t K, int bt) {
     return 3500 + (tiles * split + sms - 1) / sms * ((kb + split - 1) / split * c + 25 * std::min<int64_t>(bt, M) / split);
 }
 
-// Tokens per tile for a forward product of M rows, 0 where the pair kernel is estimated faster.
-// Up to 64 rows, where the weights are the traffic, this kernel always serves; e.g. 256 x 4096 x
+// Tokens per tile (`least` or more) for a product of M tokens, N features and K, 0 where the pair
+// kernel is estimated faster.  Forward products of up to 64 rows, where the weights are the
+// traffic, it always serves; e.g. 256 x 4096 x
 // 4096 19.3 us against 20.6 by the pair kernel, 128 x 12288 x 4096 36.7 against 32.1, 1024 x 1024
 // x 1024 9.2 against 9.3, 512 x 4096 x 4096 31.3 against 20.7.
-inline int tokens_per_tile(int64_t M, int64_t N, int64_t K) {
-    int best = 16;
-    for (int bt = 32; bt <= 128; bt *= 2)
+inline int tokens_per_tile(int64_t M, int64_t N, int64_t K, bool forward, bool plain, int least) {
+    int best = least;
+    for (int bt = 2 * least; bt <= 128; bt *= 2)
         if (cost(M, N, K, bt) < cost(M, N, K, best)) best = bt;
     if ((M + best - 1) / best > 65535) return 0;  // the grid's second dimension
-    if (M > 64 && cost(M, N, K, best) >= std::min(pair::cost(M, N, K, 128), pair::cost(M, N, K, 256))) return 0;
+    if (!(forward && M <= 64) && cost(M, N, K, best) >= std::min(pair::cost(M, N, K, 128, plain), pair::cost(M, N, K, 256, plain))) return 0;
     return best;
 }
 
-template <int ACT>
-qkn_status launch(const pair::Matrix &x, const pair::Matrix &W, const pair::Matrix &y, const pair::Matrix *res,
+// y[token][feature] = epilogue of sum_k F(feature, k) T(token, k).
+template <int ACT, bool F_MN, bool T_MN>
+qkn_status launch(const pair::Matrix &t, const pair::Matrix &f, const pair::Matrix &y, const pair::Matrix *res,
                   const pair::Matrix *z, const Epilogue &epi, int64_t K, int tokens, cudaStream_t s) {
     Args a;
     a.epi = epi;
@@ -322,10 +343,12 @@ qkn_status launch(const pair::Matrix &x, const pair::Matrix &W, const pair::Matr
     a.M = (int)y.rows;
     a.N = (int)y.inner;
     a.k_blocks = (int)((K + BK - 1) / BK);
-    if (tokens == 16) return launch_bt<16, ACT>(x, W, a, s);
-    if (tokens == 32) return launch_bt<32, ACT>(x, W, a, s);
-    if (tokens == 64) return launch_bt<64, ACT>(x, W, a, s);
-    return launch_bt<128, ACT>(x, W, a, s);
+    if constexpr (!T_MN) {
+        if (tokens == 16) return launch_bt<16, ACT, F_MN, false>(t, f, a, s);
+        if (tokens == 32) return launch_bt<32, ACT, F_MN, false>(t, f, a, s);
+    }
+    if (tokens == 64) return launch_bt<64, ACT, F_MN, T_MN>(t, f, a, s);
+    return launch_bt<128, ACT, F_MN, T_MN>(t, f, a, s);
 }
 
 }  // namespace rows

@@ -85,12 +85,16 @@ def check_forward(x, W, bias, act, res, inv, y, z, what=""):
     close(y, yr, ye, what + " y")
 
 
-# From a single token to several tiles; widths of less than a tile, one tile and ragged ones.  The
-# kernel for few rows serves them up to 700 (16, 32, 64 and 128 tokens per tile, several tiles of
-# 128 at the end, K split and whole), the pair kernel the last two: 128 columns per tile (1029) and 256 (1500).
+# From a single token to several tiles; widths of less than a tile, one tile and ragged ones.
 SIZES = [(1, 64, 64), (1, 264, 1000), (2, 8, 8), (3, 128, 72), (17, 520, 136), (64, 256, 512), (100, 1032, 264),
          (128, 128, 128), (129, 264, 1000), (256, 256, 256), (257, 520, 64), (700, 776, 200), (1029, 2056, 1000),
          (1500, 4104, 1600)]
+# One for each kernel and tile that the sizes choose between on 148 SMs: of the forward product the
+# kernel for few rows with 32, 64 and 128 tokens per tile, then the pair kernel with 128 and 256
+# columns (16 tokens are taken by the small ones above); the same of dx; of dW.
+SIZES += [(65, 3728, 8), (333, 2704, 8), (500, 3464, 8), (333, 3344, 264), (1000, 3464, 72),
+          (65, 8, 3736), (500, 8, 1696), (65, 712, 3080), (333, 264, 3336), (1000, 72, 3816),
+          (100, 8, 8), (1000, 3224, 8), (200, 3272, 264), (65, 3528, 912)]
 
 
 @pytest.mark.parametrize("act", ACTS)
