@@ -391,7 +391,9 @@ typedef enum {
  * normalised q and k take their positions next.
  *
  * q [T][dq], k [T][dk], pitches ldq, ldk; dk == 0 rotates q only.  q_out ==
- * NULL (resp. k_out == NULL) works in place.  inverse != 0 turns back (the
+ * NULL (resp. k_out == NULL) works in place.  A result that shares
+ * memory with an input in any other way, or with the other result, is refused
+ * (QKN_ERR_UNSUPPORTED); columns of one wider buffer are fine.  inverse != 0 turns back (the
  * sine's sign is flipped, mscale is still applied): the gradient of the call
  * without it.  fp32 arithmetic, one rounding to `act`.  Any element-aligned
  * pointers and pitches are accepted; 16-byte aligned rows with head_dim a
@@ -412,6 +414,8 @@ QKN_API qkn_status rotary_apply(const void *q, const void *k, void *q_out, void 
  * n is not rounded in between; y is rounded once.  rotary_dim == 0 leaves the
  * rotation out (head_dim, positions, pos_bits, inv_freq, layout and mscale
  * are then ignored).  Arguments as for qknorm_fused and rotary_apply.
+ * A row's bits do not depend on the rows beside it; the order of its sum goes
+ * by the widths of the call's tensors, their types and alignment.
  */
 QKN_API qkn_status qknorm_rotary(const void *q, const void *k, const void *wq, const void *wk,
                                  void *q_out, void *k_out, int64_t T, int64_t dq, int64_t dk,
@@ -430,8 +434,8 @@ QKN_API qkn_status qknorm_rotary(const void *q, const void *k, const void *wq, c
  *
  * dq_out [T][dq], dk_out [T][dk]  gradients of the outputs, pitches ldgq, ldgk
  * q, k, wq, wk                    the forward call's inputs
- * dq_in, dk_in                    results in `act`, pitches lddq, lddk; they
- *                                 must not overlap any input
+ * dq_in, dk_in                    results in `act`, pitches lddq, lddk; sharing
+ *                                 memory with an input is refused
  * dwq [dq], dwk [dk]              results, fp32, always written (zeros when T == 0)
  * workspace    at least qknorm_rotary_backward_workspace_bytes(T, dq, dk)
  *              bytes of device scratch, 16-byte aligned, or NULL to allocate
@@ -474,15 +478,19 @@ typedef enum {
  *
  * x         [M][K] bf16, pitch ldx
  * W         [N][K] bf16 (K contiguous), pitch ldw
- * y         [M][N] bf16, pitch ldy; must not overlap x, W or preact
+ * y         [M][N] bf16, pitch ldy; sharing memory with x, W or preact is
+ *           refused (QKN_ERR_UNSUPPORTED), columns of one wider buffer are fine
  * bias      [N] of bias_dt, or NULL
  * residual  [M][N] bf16, pitch ldr, or NULL; may be y itself (the result is
  *           then added in place)
  * inv_rms   [M] fp32 row scale (flashnorm_inv_rms, with W folded by
  *           flashnorm_fold_weights), or NULL for 1
- * preact    [M][N] bf16, pitch ldz, receives z for linear_fused_backward, or NULL
+ * preact    [M][N] bf16, pitch ldz, receives z for linear_fused_backward, or
+ *           NULL; sharing memory with x, W or residual is refused
  * M >= 0, N and K multiples of 8, each below 2^31 - 512; pitches multiples of
  * 8; x, W, y, bias, residual and preact 16-byte aligned.  One launch, nothing is allocated.
+ * The same call gives the same bits; the order in which K is added up goes by
+ * M, N and K.
  * A device-side wait that gives up is reported by qkn_check_device.
  */
 QKN_API qkn_status linear_fused(const void *x, const void *W, void *y,
@@ -501,8 +509,8 @@ QKN_API qkn_status linear_fused(const void *x, const void *W, void *y,
  *         QKN_ACT_NONE);  x, W as in the forward call
  * dx      [M][K] bf16, pitch lddx;  dW [N][K] bf16, pitch lddw;  dbias [N]
  *         fp32.  Each may be NULL and is then left out (x is read for dW, W
- *         for dx).  They must not overlap the inputs.  M == 0 writes zeros to
- *         dW and dbias
+ *         for dx).  Sharing memory with an input or with one another is refused
+ *         (QKN_ERR_UNSUPPORTED).  M == 0 writes zeros to dW and dbias
  * workspace  at least linear_fused_backward_workspace_bytes(M, N, K, act)
  *         bytes of device scratch, 16-byte aligned, or NULL to allocate it
  *         stream-ordered inside the call

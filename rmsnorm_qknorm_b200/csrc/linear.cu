@@ -143,6 +143,11 @@ qkn_status forward(const pair::Matrix &x, const pair::Matrix &W, const pair::Mat
 
 bool pitch_ok(int64_t ld, int64_t width) { return ld >= width && ld % 8 == 0; }
 
+// Whether the rows of a bf16 result share memory with those of another matrix.
+bool meets(const pair::Matrix &y, const pair::Matrix &m) {
+    return rows_overlap({y.p, y.rows, y.inner * 2, y.pitch * 2}, {m.p, m.rows, m.inner * 2, m.pitch * 2});
+}
+
 }  // namespace lin
 
 qkn_status read_linear_error(int *flag) {
@@ -185,6 +190,10 @@ extern "C" QKN_API qkn_status linear_fused(const void *x, const void *W, void *y
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const lin::pair::Matrix mx = {x, M, K, ldx}, mw = {W, N, K, ldw}, my = {y, M, N, ldy}, mr = {residual, M, N, ldr},
                             mz = {preact, M, N, ldz};
+    const bool in_place = residual == y && (M == 1 || ldr == ldy);
+    if (lin::meets(my, mx) || lin::meets(my, mw) || lin::meets(my, mz) || (lin::meets(my, mr) && !in_place) ||
+        lin::meets(mz, mx) || lin::meets(mz, mw) || lin::meets(mz, mr))
+        return fail(QKN_ERR_UNSUPPORTED, "%s: y or preact shares memory with an input or with one another", fn);
     const lin::pair::Matrix *res = residual ? &mr : nullptr, *z = preact ? &mz : nullptr;
     lin::Epilogue e{};
     e.inv_rms = inv_rms;
@@ -243,6 +252,15 @@ extern "C" QKN_API qkn_status linear_fused_backward(const void *dy, const void *
         if (dW != nullptr) e = cudaMemset2DAsync(dW, (size_t)lddw * 2, 0, (size_t)K * 2, (size_t)N, s);
         if (e == cudaSuccess && dbias != nullptr) e = cudaMemsetAsync(dbias, 0, (size_t)N * 4, s);
         return e == cudaSuccess ? QKN_OK : cuda_fail(e, "linear_fused_backward: clearing the gradients");
+    }
+    {
+        const lin::pair::Matrix results[2] = {{dx, M, K, lddx}, {dW, N, K, lddw}};
+        const lin::pair::Matrix inputs[4] = {{dy, M, N, lddy}, {has_z ? preact : nullptr, M, N, ldz},
+                                             {dW ? x : nullptr, M, K, ldx}, {dx ? W : nullptr, N, K, ldw}};
+        bool met = lin::meets(results[0], results[1]);
+        for (const lin::pair::Matrix &r : results)
+            for (const lin::pair::Matrix &m : inputs) met = met || lin::meets(r, m);
+        if (met) return fail(QKN_ERR_UNSUPPORTED, "%s: dx or dW shares memory with an input or with one another", fn);
     }
     void *own = nullptr;
     if (workspace == nullptr && (has_z || dbias != nullptr)) {

@@ -66,9 +66,13 @@ template <int GROUP> __device__ __forceinline__ void elect_commit(uint32_t bar) 
 }
 
 // mbar_wait by a whole warp: the same answer on every lane.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int *err) {
-    return __all_sync(0xffffffffu, mbar_wait_fast(bar, parity, err));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int *err, uint64_t timeout_ns = kWaitTimeoutNs) {
+    return __all_sync(0xffffffffu, mbar_wait_fast(bar, parity, err, timeout_ns));
 }
+
+// The limit of a wait for a whole product of k_blocks blocks of 64 k (at most 0.5 us each; 2^31 k
+// alone pass the usual limit).
+__device__ __forceinline__ uint64_t product_timeout(int k_blocks) { return kWaitTimeoutNs + 4000ull * (uint64_t)k_blocks; }
 
 }  // namespace lin
 }  // namespace qkn

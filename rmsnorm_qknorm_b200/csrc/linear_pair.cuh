@@ -290,7 +290,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             }
             const float r = g.epi.inv_rms != nullptr && in ? __ldg(g.epi.inv_rms + row) : 1.f;
             asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
-            if (ok) ok = warp_wait(smem_u32(&acc_full[acc]), acc_phase, &g_linear_error);
+            if (ok) ok = warp_wait(smem_u32(&acc_full[acc]), acc_phase, &g_linear_error, product_timeout(g.k_blocks));
             gemm::tc_fence_after();
             const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN + half * (BN / 2);
             for (int j = 0; ok && j < S::BOXES; ++j) {
@@ -403,7 +403,7 @@ qkn_status launch_bn(const Matrix &a, const Matrix &b, const Matrix &y, const Ma
     g.pm_blocks = (int)(((int64_t)g.M + 2 * BM - 1) / (2 * BM));
     g.n_blocks = (int)(((int64_t)g.N + BN - 1) / BN);
     g.k_blocks = (int)((K + BK - 1) / BK);
-    if ((int64_t)g.pm_blocks * g.n_blocks > 0x7fffffffLL) return fail(QKN_ERR_SHAPE, "linear_pair_kernel: too many tiles");
+    if ((int64_t)g.pm_blocks * g.n_blocks > 0x7fff0000LL) return fail(QKN_ERR_SHAPE, "linear_pair_kernel: too many tiles");
     g.num_tiles = g.pm_blocks * g.n_blocks;
     static std::atomic<int> max_pairs[64];  // per device: resident clusters of two (0 until measured)
     int dev = 0;

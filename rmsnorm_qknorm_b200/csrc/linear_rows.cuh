@@ -222,7 +222,7 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
         else load_weights_batched<float, 4>(static_cast<const float *>(g.epi.bias) + n0 + 4 * lane, bias);
     }
     // every thread: the accumulator is complete and no MMA reads the ring any more
-    mbar_wait(smem_u32(acc_full), 0u, &g_linear_error);
+    mbar_wait(smem_u32(acc_full), 0u, &g_linear_error, product_timeout(kb1 - kb0));
     gemm::tc_fence_after();
     __syncthreads();
     float *tile = reinterpret_cast<float *>(smem);  // [BT tokens][BF features]

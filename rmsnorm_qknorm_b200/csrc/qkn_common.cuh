@@ -21,6 +21,37 @@ qkn_status check_launch(const char *what);
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Rows of a call's operand or result: `rows` of `bytes`, `pitch` bytes apart.
+struct Span {
+    const void *p;
+    int64_t rows, bytes, pitch;
+};
+
+// Whether any row of a shares a byte with a row of b.  Columns of one wider buffer do not, although
+// their address ranges cross.
+inline bool rows_overlap(const Span &a, const Span &b) {
+    using wide = __int128;  // pitches are the caller's: rows * pitch may pass 64 bits
+    if (a.p == nullptr || b.p == nullptr || a.rows < 1 || b.rows < 1 || a.bytes < 1 || b.bytes < 1) return false;
+    if (a.rows > b.rows) return rows_overlap(b, a);
+    const wide b0 = (wide)reinterpret_cast<uintptr_t>(b.p) - (wide)reinterpret_cast<uintptr_t>(a.p);  // from a's start
+    if (b0 + (wide)(b.rows - 1) * b.pitch + b.bytes <= 0 || (wide)(a.rows - 1) * a.pitch + a.bytes <= b0) return false;
+    if (a.rows > 1 && a.pitch == b.pitch) {
+        const wide at = (b0 % a.pitch + a.pitch) % a.pitch;  // where b's rows begin in a's
+        return at < a.bytes || at + b.bytes > a.pitch;
+    }
+    for (int64_t i = 0; i < a.rows; ++i) {
+        const wide start = (wide)i * a.pitch, before = start - b0 - b.bytes;
+        const wide j = before < 0 ? 0 : before / b.pitch + 1;  // b's first row that ends behind the start of a's row i
+        if (j < b.rows && b0 + j * b.pitch < start + a.bytes) return true;
+    }
+    return false;
+}
+
+// The same rows: a result that replaces its operand in place.
+inline bool same_rows(const Span &a, const Span &b) {
+    return a.p == b.p && a.rows == b.rows && a.bytes == b.bytes && (a.rows <= 1 || a.pitch == b.pitch);
+}
+
 inline size_t dtype_size(qkn_dtype t) { return t == QKN_F32 ? 4 : 2; }
 
 inline bool valid_dtype(int t) { return t == QKN_F32 || t == QKN_BF16; }

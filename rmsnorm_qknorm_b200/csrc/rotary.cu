@@ -380,6 +380,23 @@ qkn_status check_rotary_pointers(const char *fn, const void *positions, int pos_
     return QKN_OK;
 }
 
+// The results are the operand's own rows (in place) or rows that share nothing with any operand,
+// and not one another's: rows are read ahead of the ones that are written.
+qkn_status check_rotary_rows(const char *fn, const Args &a, int64_t es, bool inplace) {
+    for (int i = 0; i < a.njobs; ++i) {
+        const Job &j = a.job[i];
+        const Span y = {j.y, a.T, j.d * es, j.ldy};
+        for (int o = 0; o < a.njobs; ++o) {
+            const Job &k = a.job[o];
+            const Span x = {k.x, a.T, k.d * es, k.ldx}, g = {k.g, a.T, k.d * es, k.ldg}, z = {k.y, a.T, k.d * es, k.ldy};
+            if ((rows_overlap(y, x) && !(inplace && o == i && same_rows(y, x))) || rows_overlap(y, g) ||
+                (o > i && rows_overlap(y, z)))
+                return fail(QKN_ERR_UNSUPPORTED, "%s: a result shares memory with an input or the other result", fn);
+        }
+    }
+    return QKN_OK;
+}
+
 }  // namespace rot
 }  // namespace qkn
 
@@ -411,6 +428,7 @@ extern "C" QKN_API qkn_status rotary_apply(const void *q, const void *k, void *q
     a.job[1] = {static_cast<const uint8_t *>(k), nullptr, static_cast<uint8_t *>(k_out ? k_out : const_cast<void *>(k)),
                 nullptr, nullptr, ldk * e, 0, (k_out ? ldk_out : ldk) * e, (int)dk};
     a.njobs = has_k ? 2 : 1;
+    if (qkn_status st = rot::check_rotary_rows(fn, a, e, true)) return st;
     return rot::launch_types<rot::kRotate>(a, act, act, static_cast<cudaStream_t>(stream));
 }
 
@@ -443,6 +461,7 @@ extern "C" QKN_API qkn_status qknorm_rotary(const void *q, const void *k, const 
     a.job[1] = {static_cast<const uint8_t *>(k), nullptr, static_cast<uint8_t *>(k_out ? k_out : const_cast<void *>(k)),
                 wk, nullptr, ldk * e, 0, (k_out ? ldk_out : ldk) * e, (int)dk};
     a.njobs = has_k ? 2 : 1;
+    if (qkn_status st = rot::check_rotary_rows(fn, a, e, true)) return st;
     return rot::launch_types<rot::kNorm>(a, act, wdt, static_cast<cudaStream_t>(stream));
 }
 
@@ -495,12 +514,6 @@ extern "C" QKN_API qkn_status qknorm_rotary_backward(
         if (e == cudaSuccess && has_k) e = cudaMemsetAsync(dwk, 0, (size_t)dk * 4, s);
         return e == cudaSuccess ? QKN_OK : cuda_fail(e, "qknorm_rotary_backward: clearing the weight gradients");
     }
-    void *own = nullptr;
-    if (workspace == nullptr) {
-        const cudaError_t e = cudaMallocAsync(&own, need, s);
-        if (e != cudaSuccess) return cuda_fail(e, "qknorm_rotary_backward: workspace");
-        workspace = own;
-    }
     rot::Args a{};
     rot::fill(a, T, head_dim, positions, pos_bits, inv_freq, rotary_dim, (int)layout, mscale, true, eps);
     const int64_t e = (int64_t)dtype_size(act);
@@ -509,6 +522,13 @@ extern "C" QKN_API qkn_status qknorm_rotary_backward(
     a.job[1] = {static_cast<const uint8_t *>(k), static_cast<const uint8_t *>(dk_out), static_cast<uint8_t *>(dk_in), wk,
                 dwk, ldk * e, ldgk * e, lddk * e, (int)dk};
     a.njobs = has_k ? 2 : 1;
+    if (qkn_status st = rot::check_rotary_rows(fn, a, e, false)) return st;
+    void *own = nullptr;
+    if (workspace == nullptr) {
+        const cudaError_t f = cudaMallocAsync(&own, need, s);
+        if (f != cudaSuccess) return cuda_fail(f, "qknorm_rotary_backward: workspace");
+        workspace = own;
+    }
     a.inv = static_cast<float *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ((size_t)T * 2 * 4 + 255) / 256 * 256);
     qkn_status st = rot::launch_types<rot::kNormBack>(a, act, wdt, s);

@@ -50,6 +50,8 @@ def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str | No
             raise ValueError("yarn scaling needs the original length")
         if not fast > slow > 0:
             raise ValueError("yarn scaling needs fast > slow > 0")
+        if original < slow * 2 * math.pi:
+            raise ValueError("yarn scaling needs an original length over which the fastest pair turns `slow` times")
         # the (fractional) pair that turns n times over the original length
         low, high = (r * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow))
         low, high = max(math.floor(low), 0), min(math.ceil(high), r - 1)

@@ -69,3 +69,19 @@ def test_binding_refusals():
         qk.linear_fused_backward(torch.zeros(4, 64, dtype=torch.bfloat16), x, W)
     with pytest.raises(ValueError, match="act"):
         qk.linear_fused_backward_workspace_bytes(4, 64, 32, "tanh")
+
+
+@pytest.mark.parametrize("kw", [dict(y=P), dict(W=4 * P, y=4 * P), dict(W=4 * P, y=8 * P, z=8 * P, ldz=64),
+                                dict(W=4 * P, y=8 * P, res=8 * P + 16, ldr=64),     # a shifted residual
+                                dict(W=4 * P, y=8 * P, res=8 * P, ldr=72),          # in place, another pitch
+                                dict(W=4 * P, y=8 * P, z=P, ldz=64), dict(W=4 * P, y=8 * P, z=4 * P + 4000, ldz=64),
+                                dict(W=4 * P, y=8 * P, z=16 * P, ldz=64, res=16 * P, ldr=64),
+                                dict(x=P, ldx=128, W=4 * P, y=P + 32, ldy=128)])    # columns that cross x's
+def test_results_over_inputs_are_refused(lib, kw):
+    assert lin(lib, **kw) == UNSUP
+    assert "shares memory" in lib.qkn_last_error().decode()
+
+
+@pytest.mark.parametrize("kw", [dict(dx=P), dict(dx=2 * P, dW=P), dict(dx=2 * P, dW=2 * P), dict(dx=2 * P, dW=2 * P + 256)])
+def test_gradients_over_inputs_are_refused(lib, kw):
+    assert back(lib, **kw) == UNSUP

@@ -279,3 +279,44 @@ def test_refusals_of_the_binding(cuda_lib):
                      ((z, x, W), dict(dx_out=z)), ((z, x, None), dict(dx_out=x))):
         with pytest.raises(ValueError):
             qk.linear_fused_backward(*args, **kw)
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 136, 72), (333, 3344, 264)])  # the kernel for few rows, the pair kernel
+def test_offsets_beyond_32_bits(cuda_lib, M, N, K):
+    # every operand but W is a block of columns of one buffer whose rows lie so far apart that the
+    # last ones pass 2^32 bytes; the same bits as contiguous operands
+    pitch = (2 ** 31 // (M - 1) + 64) // 8 * 8
+    buf = torch.empty(M, pitch, dtype=torch.bfloat16, device=DEV)
+    x, dx = buf[:, :K], buf[:, 512: 512 + K]
+    dy, y, z = (buf[:, c: c + N] for c in (1024, 5120, 9216))
+    assert M * pitch * 2 > 2 ** 32
+    W = normal(N, K, seed=2)
+    x.copy_(normal(M, K, seed=1))
+    dy.copy_(normal(M, N, seed=3))
+    y.copy_(dy)
+    qk.linear_fused(x, W, None, "gelu", y, preact_out=z, out=y)
+    _, dW, _ = qk.linear_fused_backward(dy, x, W, z, "gelu", dx_out=dx)
+    xc, dyc, zc = x.contiguous(), dy.contiguous(), torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    assert torch.equal(qk.linear_fused(xc, W, None, "gelu", dyc, preact_out=zc), y) and torch.equal(z, zc)
+    gx, gW, _ = qk.linear_fused_backward(dyc, xc, W, zc, "gelu")
+    assert torch.equal(dx, gx) and torch.equal(dW, gW)
+
+
+def test_a_long_sum_of_ones_is_exact(cuda_lib):
+    # 2^24 rows: every partial sum of ones is an integer that fp32 holds, in whatever order
+    M = 2 ** 24
+    dy, x = (torch.ones(M, 8, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    _, dW, db = qk.linear_fused_backward(dy, x, None, need_dbias=True)
+    assert bool((dW == M).all()) and bool((db == M).all())
+
+
+def test_results_of_columns_beside_the_inputs(cuda_lib):
+    # columns of one buffer under two pitches (every row of one, every other row of the other)
+    M, N, K = 6, 64, 64
+    buf = normal(2 * M, 256, seed=1)
+    x, W = buf[::2, :K], normal(N, K, seed=2, scale=0.1)
+    ref = qk.linear_fused(x.contiguous(), W)
+    y = buf[:M, 128: 128 + N]
+    assert torch.equal(qk.linear_fused(x, W, out=y), ref)
+    with pytest.raises(qk.QKNormError, match="shares memory"):
+        qk.linear_fused(x, W, out=buf[:M, 56: 56 + N])

@@ -115,3 +115,26 @@ def test_binding_refuses_cpu_tensors_and_wrong_arguments():
         qk.qknorm_rotary(x, None, torch.ones(64), None, pos, f, 64)
     with pytest.raises(ValueError, match="CUDA"):
         qk.qknorm_rotary_backward(x, None, x, None, torch.ones(64), None, pos, f, 64)
+
+
+def test_yarn_refuses_a_length_without_a_slow_turn():
+    with pytest.raises(ValueError, match="original length"):
+        qk.rotary_inv_freq(8, scaling="yarn", factor=2.0, original=6, device="cpu")
+
+
+# Results over inputs, other than a result in place of its own operand.  Row width 128 (q) and 64 (k) bf16.
+@pytest.mark.parametrize("kw", [dict(q=P, k=P, qo=None, ko=None),                  # one tensor twice, in place
+                                dict(q=P, k=P + 128, qo=None, ko=None),            # k's columns among q's
+                                dict(q=P, k=4 * P, qo=2 * P, ko=2 * P),            # one result for both
+                                dict(q=P, k=4 * P, qo=4 * P, ko=8 * P),            # q's result over k
+                                dict(q=P, k=4 * P, qo=P + 256, ko=8 * P),          # a row further down
+                                dict(q=P, k=4 * P, qo=P, ldqo=136, ko=8 * P),      # in place with another pitch
+                                dict(q=P, k=4 * P, qo=2 * P, ko=2 * P + 256, ldqo=256, ldko=200)])
+def test_results_over_inputs_are_refused(lib, kw):
+    assert rot(lib, **kw) == UNSUP
+    assert "shares memory" in lib.qkn_last_error().decode()
+
+
+def test_gradients_over_inputs_are_refused(lib):
+    for kw in (dict(dqi=P), dict(gq=P, q=4 * P, dqi=4 * P), dict(gq=P, q=4 * P, dqi=P + 512)):
+        assert back(lib, **kw) == UNSUP, kw

@@ -414,3 +414,37 @@ def test_refusals_of_the_binding(cuda_lib):
         qk.qknorm_rotary_backward(*back, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError, match="gk"):
         qk.qknorm_rotary_backward(d["gq"], None, *back[2:])
+
+
+@pytest.mark.parametrize("shift", [0, 1])  # the unit kernel, the element-wise kernels
+def test_offsets_beyond_32_bits(cuda_lib, shift):
+    # the rows of every operand are columns of one buffer, so far apart that the last ones pass 2^32 bytes
+    T, hq, hk, D = 9, 4, 2, 64
+    s = make(T, hq, hk, D, 64, torch.bfloat16, seed=5)
+    d = dev(s)
+    pitch = 2 ** 28 + 8 + shift
+    buf = torch.empty(T, pitch, dtype=torch.bfloat16, device=DEV)
+    at = lambda c, w: buf[:, c: c + w]  # noqa: E731
+    v = {n: at(512 * i, d[n].shape[1]) for i, n in enumerate(("q", "k", "gq", "gk"))}
+    o = [at(512 * i, w * D) for i, w in ((4, hq), (5, hk), (6, hq), (7, hk))]
+    for n, t in v.items():
+        t.copy_(d[n])
+    # the same alignment in a small buffer: the same kernel, the same bits
+    small = {n: torch.empty(T, 512 + shift, dtype=torch.bfloat16, device=DEV)[:, : t.shape[1]].copy_(t) for n, t in v.items()}
+    rest = (d["pos"], d["freq"], D)
+    for call in (lambda a, **kw: qk.rotary_apply(a["q"], a["k"], *rest, **kw),
+                 lambda a, **kw: qk.qknorm_rotary(a["q"], a["k"], d["wq"], d["wk"], *rest, **kw)):
+        got, want = call(v, q_out=o[0], k_out=o[1]), call(small)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    want = qk.qknorm_rotary_backward(small["gq"], small["gk"], small["q"], small["k"], d["wq"], d["wk"], *rest)
+    got = qk.qknorm_rotary_backward(v["gq"], v["gk"], v["q"], v["k"], d["wq"], d["wk"], *rest, dq_out=o[2], dk_out=o[3])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_one_tensor_twice_is_refused_in_place(cuda_lib):
+    s = dev(make(5, 2, 2, 64, 64, torch.bfloat16, seed=6))
+    with pytest.raises(qk.QKNormError, match="shares memory"):
+        qk.rotary_apply(s["q"], s["q"], s["pos"], s["freq"], 64, inplace=True)
+    a, b = qk.rotary_apply(s["q"], s["q"], s["pos"], s["freq"], 64)
+    assert torch.equal(a, b)
