@@ -396,8 +396,8 @@ typedef enum {
  * (QKN_ERR_UNSUPPORTED); columns of one wider buffer are fine.  inverse != 0 turns back (the
  * sine's sign is flipped, mscale is still applied): the gradient of the call
  * without it.  fp32 arithmetic, one rounding to `act`.  Any element-aligned
- * pointers and pitches are accepted; 16-byte aligned rows with head_dim a
- * multiple of 16 bytes and rotary_dim of 32 bytes take the fast kernel.
+ * pointers and pitches are accepted; 16-byte aligned rows of whole 16 bytes
+ * with head_dim a multiple of 4 and rotary_dim of 8 take the fast kernel.
  */
 QKN_API qkn_status rotary_apply(const void *q, const void *k, void *q_out, void *k_out,
                                 int64_t T, int64_t dq, int64_t dk,

@@ -16,8 +16,9 @@
 // token's critical path.)
 //
 // A consumer thread owns the same columns of every token: UPT "units" of two
-// 16-byte chunks, chunk j and chunk j + r / 2E of a head (E elements per
-// chunk).  In the half layout the two chunks hold the two sides of E pairs;
+// chunks, chunk j and chunk j + r / 2E of a head (E elements per chunk, 16
+// bytes of them, or 8 where the rotated part of a bf16 head is a multiple of
+// 16 but not of 32 bytes).  In the half layout the two chunks hold the two sides of E pairs;
 // in the interleaved layout each holds E / 2 whole pairs.  Either way a unit
 // needs the cos and sin of two runs of E / 2 frequencies, which the table
 // keeps at positions j and j + r / 2E (filled in the order the layout asks
@@ -125,24 +126,35 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
-// A 16-byte chunk as E / 2 pairs of fp32.
-template <typename TA, int H> __device__ __forceinline__ void unpack2(const uint4 &v, float2 (&f)[H]) {
+// A chunk in shared memory as E / 2 = H pairs of fp32 (16 bytes, or 8: four bf16).
+template <typename TA, int H> __device__ __forceinline__ void lds_chunk(uint32_t addr, float2 (&f)[H]) {
     if constexpr (sizeof(TA) == 4) {
+        const uint4 v = lds128(addr);
         f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
         f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+    } else if constexpr (H == 2) {
+        uint2 v;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+        f[0] = make_float2(bf16lo(v.x), bf16hi(v.x));
+        f[1] = make_float2(bf16lo(v.y), bf16hi(v.y));
     } else {
+        const uint4 v = lds128(addr);
         f[0] = make_float2(bf16lo(v.x), bf16hi(v.x));
         f[1] = make_float2(bf16lo(v.y), bf16hi(v.y));
         f[2] = make_float2(bf16lo(v.z), bf16hi(v.z));
         f[3] = make_float2(bf16lo(v.w), bf16hi(v.w));
     }
 }
-template <typename TA, int H> __device__ __forceinline__ uint4 pack2(const float2 (&f)[H]) {
+template <typename TA, int H> __device__ __forceinline__ void store_chunk(uint8_t *p, const float2 (&f)[H]) {
     if constexpr (sizeof(TA) == 4)
-        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+        st_stream_batched(p, make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                                        __float_as_uint(f[1].y)));
+    else if constexpr (H == 2)
+        asm("st.global.cs.v2.u32 [%0], {%1, %2};"
+            ::"l"(p), "r"(pack_bf16x2(f[0].x, f[0].y)), "r"(pack_bf16x2(f[1].x, f[1].y)) : "memory");
     else
-        return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
-                          pack_bf16x2(f[3].x, f[3].y));
+        st_stream_batched(p, make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                                        pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y)));
 }
 
 // H = E / 2 consecutive floats of the table, as pairs.
@@ -250,10 +262,10 @@ enum Shape {
     MULTI   // one warp serves both tensors of several tokens at a time
 };
 
-template <typename TA, int MODE, int UPT, bool HALF, int SHAPE>
-__global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rotary_unit_kernel(const Params a) {
+template <typename TA, int E, int MODE, int UPT, bool HALF, int SHAPE>
+__global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_kernel(const Params a) {
     constexpr bool BOTH = SHAPE != SPLIT, BATCH = SHAPE == MULTI;
-    constexpr int E = Chunk<TA>::E, H = E / 2;
+    constexpr int H = E / 2, CB = E * (int)sizeof(TA);  // bytes of a chunk
     constexpr bool NORM = MODE != kRotate, BACK = MODE == kNormBack;
     extern __shared__ __align__(128) uint8_t smem[];
     const int gthreads = (a.warps + 1) * 32;
@@ -319,7 +331,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
         }
     }
     for (int i = gt; i < 8 * kSlots; i += gthreads) red[i] = 0.f;
-    const int chunks0 = a.job[0].row_bytes / 16, chunks = a.x_bytes / 16;
+    const int chunks0 = a.job[0].row_bytes / CB, chunks = a.x_bytes / CB;
     if (threadIdx.x < 4) reinterpret_cast<float *>(smem)[NORM ? chunks * E + threadIdx.x : threadIdx.x] = 0.f;  // zeros
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -430,13 +442,13 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
             const int h = u / J.units_per_head, j = u - h * J.units_per_head;
             const int first = h * J.head_chunks;
             if (j < a.rot_units) {
-                off_a[i] = J.row_off + (first + j) * 16;
-                off_b[i] = off_a[i] + a.rot_units * 16;
+                off_a[i] = J.row_off + (first + j) * CB;
+                off_b[i] = off_a[i] + a.rot_units * CB;
                 tab[i] = j * H * 4;
             } else {
                 const int t = j - a.rot_units;
-                off_a[i] = J.row_off + (first + 2 * a.rot_units + t) * 16;
-                if (t + J.tail_units < J.tail_chunks) off_b[i] = off_a[i] + J.tail_units * 16;
+                off_a[i] = J.row_off + (first + 2 * a.rot_units + t) * CB;
+                if (t + J.tail_units < J.tail_chunks) off_b[i] = off_a[i] + J.tail_units * CB;
             }
         }
         if constexpr (BACK) {
@@ -480,20 +492,20 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
             for (int i = 0; i < UPT; ++i) {
                 const bool has_a = live && off_a[i] >= 0, has_b = live && off_b[i] >= 0;
                 const uint32_t pa = has_a ? src + off_a[i] : zeros, pb = has_b ? src + off_b[i] : zeros;
-                const uint32_t qa = w_s + max(off_a[i], 0), qb = w_s + max(off_b[i], 0);
+                const uint32_t qa = w_s + max(off_a[i], 0) * (16 / CB), qb = w_s + max(off_b[i], 0) * (16 / CB);
                 const int m = BOTH ? (is_k >> i) & 1u : 0;
                 if constexpr (MODE == kRotate) {
-                    unpack2<TA, H>(lds128(pa), va[i]);
-                    unpack2<TA, H>(lds128(pb), vb[i]);
+                    lds_chunk<TA, H>(pa, va[i]);
+                    lds_chunk<TA, H>(pb, vb[i]);
                 } else if constexpr (MODE == kNorm) {
                     float2 q = both(0.f), w[H];
-                    unpack2<TA, H>(lds128(pa), va[i]);
+                    lds_chunk<TA, H>(pa, va[i]);
                     lds_weights<H>(qa, upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) q = __ffma2_rn(va[i][p], va[i][p], q);
 #pragma unroll
                     for (int p = 0; p < H; ++p) va[i][p] = __fmul2_rn(va[i][p], w[p]);
-                    unpack2<TA, H>(lds128(pb), vb[i]);
+                    lds_chunk<TA, H>(pb, vb[i]);
                     lds_weights<H>(qb, upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) q = __ffma2_rn(vb[i][p], vb[i][p], q);
@@ -502,21 +514,21 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
                     if (m) sq[1] = __fadd2_rn(sq[1], q);
                     else sq[0] = __fadd2_rn(sq[0], q);
                 } else {
-                    unpack2<TA, H>(lds128(has_a ? pa + g_off : zeros), va[i]);
-                    unpack2<TA, H>(lds128(has_b ? pb + g_off : zeros), vb[i]);
+                    lds_chunk<TA, H>(has_a ? pa + g_off : zeros, va[i]);
+                    lds_chunk<TA, H>(has_b ? pb + g_off : zeros, vb[i]);
                     if (tab[i] >= 0) {
                         cs.load(tab_s + tab[i], run, sin_off);
                         turn<H, HALF, false>(va[i], vb[i], cs, 1.f);
                     }
                     float2 q = both(0.f), r = both(0.f), w[H], x[H];
-                    unpack2<TA, H>(lds128(pa), x);
+                    lds_chunk<TA, H>(pa, x);
                     lds_weights<H>(qa, upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) {
                         q = __ffma2_rn(x[p], x[p], q);
                         r = __ffma2_rn(__fmul2_rn(x[p], va[i][p]), w[p], r);
                     }
-                    unpack2<TA, H>(lds128(pb), x);
+                    lds_chunk<TA, H>(pb, x);
                     lds_weights<H>(qb, upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) {
@@ -583,22 +595,22 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
                 if constexpr (BACK) {
                     const float2 nc = both(-(m ? ck : cq)), inv2 = both(inv);
                     float2 w[H], x[H];
-                    unpack2<TA, H>(lds128(has_a ? src + off_a[i] : zeros), x);
-                    lds_weights<H>(w_s + max(off_a[i], 0), upper, w);
+                    lds_chunk<TA, H>(has_a ? src + off_a[i] : zeros, x);
+                    lds_weights<H>(w_s + max(off_a[i], 0) * (16 / CB), upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) {
                         da[i][p] = __ffma2_rn(va[i][p], __fmul2_rn(x[p], inv2), da[i][p]);
                         va[i][p] = __fmul2_rn(inv2, __ffma2_rn(x[p], nc, __fmul2_rn(w[p], va[i][p])));
                     }
-                    if (has_a) st_stream_batched(y + off_a[i], pack2<TA, H>(va[i]));
-                    unpack2<TA, H>(lds128(has_b ? src + off_b[i] : zeros), x);
-                    lds_weights<H>(w_s + max(off_b[i], 0), upper, w);
+                    if (has_a) store_chunk<TA, H>(y + off_a[i], va[i]);
+                    lds_chunk<TA, H>(has_b ? src + off_b[i] : zeros, x);
+                    lds_weights<H>(w_s + max(off_b[i], 0) * (16 / CB), upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) {
                         db[i][p] = __ffma2_rn(vb[i][p], __fmul2_rn(x[p], inv2), db[i][p]);
                         vb[i][p] = __fmul2_rn(inv2, __ffma2_rn(x[p], nc, __fmul2_rn(w[p], vb[i][p])));
                     }
-                    if (has_b) st_stream_batched(y + off_b[i], pack2<TA, H>(vb[i]));
+                    if (has_b) store_chunk<TA, H>(y + off_b[i], vb[i]);
                 } else {
                     if (tab[i] >= 0) {
                         if (!same) cs.load(tab_s + tab[i], run, sin_off);
@@ -610,8 +622,8 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
                             vb[i][p] = __fmul2_rn(vb[i][p], both(inv));
                         }
                     }
-                    if (has_a) st_stream_batched(y + off_a[i], pack2<TA, H>(va[i]));
-                    if (has_b) st_stream_batched(y + off_b[i], pack2<TA, H>(vb[i]));
+                    if (has_a) store_chunk<TA, H>(y + off_a[i], va[i]);
+                    if (has_b) store_chunk<TA, H>(y + off_b[i], vb[i]);
                 }
             }
             yq += yq_step;
@@ -650,11 +662,11 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, Chunk<TA>::E>(), 1) rot
                 if (off_a[i] < 0) continue;
                 const bool k = (is_k >> i) & 1u;
                 const int col = k ? dq : 0, ro = k ? a.job[1].row_off : 0;
-                float2 *pa = reinterpret_cast<float2 *>(mine + col + (off_a[i] - ro) / 16 * E);
+                float2 *pa = reinterpret_cast<float2 *>(mine + col + (off_a[i] - ro) / CB * E);
 #pragma unroll
                 for (int p = 0; p < H; ++p) pa[p] = da[i][p];
                 if (off_b[i] >= 0) {
-                    float2 *pb = reinterpret_cast<float2 *>(mine + col + (off_b[i] - ro) / 16 * E);
+                    float2 *pb = reinterpret_cast<float2 *>(mine + col + (off_b[i] - ro) / CB * E);
 #pragma unroll
                     for (int p = 0; p < H; ++p) pb[p] = db[i][p];
                 }
@@ -683,9 +695,8 @@ struct Plan {
 
 // Whether the unit kernel takes the call, and its geometry: a rule on the
 // rows' widths, types and alignment, never on the number of tokens.
-template <typename TA, int MODE>
+template <typename TA, int E, int MODE>
 Plan plan(const Args &a, Params &p, size_t w_size) {
-    constexpr int E = Chunk<TA>::E;
     Plan r{};
     p.x_bytes = 0;
     for (int i = 0; i < a.njobs; ++i) {
@@ -706,6 +717,7 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
         J.ldy = j.ldy;
         J.d = j.d;
         J.row_bytes = j.d * (int)sizeof(TA);
+        if (J.row_bytes % 16 != 0) return r;
         J.row_off = p.x_bytes;
         p.x_bytes += J.row_bytes;
         J.head_chunks = D / E;
@@ -724,7 +736,7 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
     // another's barriers: 16384 x (5120 + 1024) bf16, gradients 145 against 118 us, rotary alone 93
     // against 67.)  Warps serve both tensors where nothing is summed over a row, or where one warp
     // is enough.
-    constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
+    constexpr int kUsual = 16 / E;
     const int most = MODE == kNormBack ? kUsual : 4;
     r.upt = kUsual;
     r.mixed = MODE == kRotate || u0 + u1 <= 32 * kUsual;
@@ -745,9 +757,9 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
     return r;
 }
 
-template <typename TA, int MODE, int UPT, bool HALF, int SHAPE>
+template <typename TA, int E, int MODE, int UPT, bool HALF, int SHAPE>
 qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bool *taken) {
-    const auto kernel = rotary_unit_kernel<TA, MODE, UPT, HALF, SHAPE>;
+    const auto kernel = rotary_unit_kernel<TA, E, MODE, UPT, HALF, SHAPE>;
     static std::atomic<bool> attr_set[64];
     int dev = 0;
     cudaGetDevice(&dev);
@@ -781,17 +793,17 @@ qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bo
     return check_launch("rotary_unit_kernel launch");
 }
 
-template <typename TA, int MODE, int UPT, int SHAPE>
+template <typename TA, int E, int MODE, int UPT, int SHAPE>
 qkn_status launch_layout(Params &p, const Plan &r, int layout, int *grid, cudaStream_t s, bool *taken) {
-    return layout == QKN_ROTARY_HALF ? launch_kernel<TA, MODE, UPT, true, SHAPE>(p, r, grid, s, taken)
-                                     : launch_kernel<TA, MODE, UPT, false, SHAPE>(p, r, grid, s, taken);
+    return layout == QKN_ROTARY_HALF ? launch_kernel<TA, E, MODE, UPT, true, SHAPE>(p, r, grid, s, taken)
+                                     : launch_kernel<TA, E, MODE, UPT, false, SHAPE>(p, r, grid, s, taken);
 }
 
 // Launches the unit kernel when it takes the call (*taken); *grid is its number of blocks.
-template <typename TA, typename TW, int MODE>
-qkn_status launch(const Args &a, bool *taken, int *grid, cudaStream_t s) {
+template <typename TA, typename TW, int E, int MODE>
+qkn_status launch_chunks(const Args &a, bool *taken, int *grid, cudaStream_t s) {
     Params p{};
-    const Plan r = plan<TA, MODE>(a, p, sizeof(TW));
+    const Plan r = plan<TA, E, MODE>(a, p, sizeof(TW));
     *taken = r.fits;
     if (!r.fits) return QKN_OK;
     p.njobs = a.njobs;
@@ -812,17 +824,26 @@ qkn_status launch(const Args &a, bool *taken, int *grid, cudaStream_t s) {
     p.wait_ns = kWaitTimeoutNs;
     p.w_bf16 = sizeof(TW) == 2;
     p.w_bytes = (MODE == kRotate ? 0 : (p.job[0].d + p.job[1].d) * 4) + 16;  // 16 bytes of zeros
-    constexpr int kUsual = sizeof(TA) == 4 ? 4 : 2;
-    if (r.tokens > 1) return launch_layout<TA, MODE, kUsual, MULTI>(p, r, a.layout, grid, s, taken);
+    constexpr int kUsual = 16 / E;
+    if (r.tokens > 1) return launch_layout<TA, E, MODE, kUsual, MULTI>(p, r, a.layout, grid, s, taken);
     if constexpr (MODE == kRotate) {
-        if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, MIXED>(p, r, a.layout, grid, s, taken);
-        if constexpr (kUsual < 4) return launch_layout<TA, MODE, 4, MIXED>(p, r, a.layout, grid, s, taken);
+        if (r.upt == kUsual) return launch_layout<TA, E, MODE, kUsual, MIXED>(p, r, a.layout, grid, s, taken);
+        if constexpr (kUsual < 4) return launch_layout<TA, E, MODE, 4, MIXED>(p, r, a.layout, grid, s, taken);
     } else {
-        if (r.mixed) return launch_layout<TA, MODE, kUsual, MIXED>(p, r, a.layout, grid, s, taken);
-        if (r.upt == kUsual) return launch_layout<TA, MODE, kUsual, SPLIT>(p, r, a.layout, grid, s, taken);
-        if constexpr (MODE == kNorm && kUsual < 4) return launch_layout<TA, MODE, 4, SPLIT>(p, r, a.layout, grid, s, taken);
+        if (r.mixed) return launch_layout<TA, E, MODE, kUsual, MIXED>(p, r, a.layout, grid, s, taken);
+        if (r.upt == kUsual) return launch_layout<TA, E, MODE, kUsual, SPLIT>(p, r, a.layout, grid, s, taken);
+        if constexpr (MODE == kNorm && kUsual < 4) return launch_layout<TA, E, MODE, 4, SPLIT>(p, r, a.layout, grid, s, taken);
     }
     return fail(QKN_ERR_UNSUPPORTED, "rotary_unit_kernel: no variant for these rows");
+}
+
+// Chunks of 16 bytes, or of 8 where only those divide the heads and their rotated part.
+template <typename TA, typename TW, int MODE>
+qkn_status launch(const Args &a, bool *taken, int *grid, cudaStream_t s) {
+    const qkn_status st = launch_chunks<TA, TW, Chunk<TA>::E, MODE>(a, taken, grid, s);
+    if constexpr (sizeof(TA) == 2)
+        if (st == QKN_OK && !*taken) return launch_chunks<TA, TW, 4, MODE>(a, taken, grid, s);
+    return st;
 }
 
 }  // namespace unit

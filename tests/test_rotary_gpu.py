@@ -120,6 +120,8 @@ def freqs(s):
 # without a multiple of 16 bytes (element-wise kernel), one head, rows of several widths
 SHAPES = [(2, 1, 64, 64), (5, 2, 128, 64), (32, 8, 128, 128), (3, 3, 80, 32), (1, 0, 256, 256), (4, 1, 96, 48),
           (3, 2, 20, 12), (2, 2, 6, 2), (40, 40, 128, 128), (7, 1, 24, 16), (1, 1, 16, 16), (3, 0, 32, 16)]
+# in bf16 16-byte rows of which only 8-byte pieces divide the heads and their rotated parts
+SHAPES += [(3, 2, 80, 40), (20, 4, 80, 40), (64, 64, 80, 40), (4, 2, 20, 8), (2, 2, 12, 8), (1, 1, 40, 24)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
