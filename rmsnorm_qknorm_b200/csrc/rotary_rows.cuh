@@ -1,5 +1,5 @@
-// Unit kernel of the rotary entry points: rows of 16-byte chunks, persistent,
-// fed by bulk copies.
+// Unit kernel of the rotary entry points: rows of 16- or 8-byte chunks,
+// persistent, fed by bulk copies.
 //
 // Included by rotary.cu only (one translation unit: its device error word,
 // Args and helpers).
@@ -18,7 +18,8 @@
 // A consumer thread owns the same columns of every token: UPT "units" of two
 // chunks, chunk j and chunk j + r / 2E of a head (E elements per chunk, 16
 // bytes of them, or 8 where the rotated part of a bf16 head is a multiple of
-// 16 but not of 32 bytes).  In the half layout the two chunks hold the two sides of E pairs;
+// 16 but not of 32 bytes).  In the half layout the two chunks hold the two
+// sides of E pairs;
 // in the interleaved layout each holds E / 2 whole pairs.  Either way a unit
 // needs the cos and sin of two runs of E / 2 frequencies, which the table
 // keeps at positions j and j + r / 2E (filled in the order the layout asks
@@ -72,6 +73,8 @@ struct Params {
     int warps0;              // consumer warps of job 0 (== warps when one warp serves both jobs)
     int stages, stage_bytes, x_bytes;  // x_bytes: the rows of one token
     int tokens, lanes;       // tokens per stage (a power of two), lanes per token
+    int table;               // floats of a token's table: cos, sin and, where units are flipped, -sin
+    int flip;                // units with this bit in their number take their chunks in the other order (0: none)
     int w_bytes, w_bf16;     // the block's fp32 copy of the weights, in front of the rings; their type in memory
     uint64_t wait_ns;
 };
@@ -79,10 +82,10 @@ struct Params {
 constexpr int kMaxWarps = 15;  // consumer warps per group
 constexpr int kSlots = 16;     // sums per tensor and token
 
-inline __host__ __device__ int table_bytes(int r) { return (r * 4 + 15) / 16 * 16; }  // cos and sin of a token
+inline __host__ __device__ int table_bytes(int floats) { return (floats * 4 + 15) / 16 * 16; }  // of a stage
 // per group: tables, 2 tokens x 2 tensors x (sum x^2, sum w g x) x kSlots sums, full and empty barriers
-inline __host__ __device__ int group_fixed(int r, int stages) {
-    return stages * table_bytes(r) + 8 * kSlots * 4 + stages * 16;
+inline __host__ __device__ int group_fixed(int floats, int stages) {
+    return stages * table_bytes(floats) + 8 * kSlots * 4 + stages * 16;
 }
 
 __device__ __forceinline__ Rows pick(const Params &a, int which) {
@@ -216,9 +219,11 @@ __device__ __forceinline__ void turn(float2 (&a)[H], float2 (&b)[H], const Turns
     }
 }
 
-// The weights of a chunk from shared memory, as pairs.  They are kept as fp32,
-// the first four of every chunk in one array and, for chunks of eight, the
-// others `upper` bytes behind: neighbouring threads read neighbouring words.
+// The weights of a unit's chunk from shared memory, as pairs.  They are kept as
+// fp32, the first four of every chunk in one array and, for chunks of eight,
+// the others `upper` bytes behind: neighbouring threads read neighbouring
+// words.  The chunks lie in the row's order, or (ORDERED) in the units', all
+// first chunks before all second ones.
 template <int H>
 __device__ __forceinline__ void lds_weights(uint32_t addr, uint32_t upper, float2 (&f)[H]) {
     const uint4 a = lds128(addr);
@@ -262,7 +267,8 @@ enum Shape {
     MULTI   // one warp serves both tensors of several tokens at a time
 };
 
-template <typename TA, int E, int MODE, int UPT, bool HALF, int SHAPE>
+// ORDERED: for heads in which units next to one another meet in shared memory's banks (see ordered_of).
+template <typename TA, int E, int MODE, int UPT, bool HALF, int SHAPE, bool ORDERED>
 __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_kernel(const Params a) {
     constexpr bool BOTH = SHAPE != SPLIT, BATCH = SHAPE == MULTI;
     constexpr int H = E / 2, CB = E * (int)sizeof(TA);  // bytes of a chunk
@@ -272,9 +278,9 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
     const int group = threadIdx.x / gthreads, gt = threadIdx.x - group * gthreads;  // thread within its group
     const int lane = threadIdx.x & 31, gw = gt >> 5;
     uint8_t *rings = smem + a.w_bytes;
-    uint8_t *fix_p = rings + (size_t)a.groups * a.stages * a.stage_bytes + (size_t)group * group_fixed(a.r * a.tokens, a.stages);
+    uint8_t *fix_p = rings + (size_t)a.groups * a.stages * a.stage_bytes + (size_t)group * group_fixed(a.table * a.tokens, a.stages);
     const uint32_t ring = smem_u32(rings + (size_t)group * a.stages * a.stage_bytes);
-    const int tbytes = table_bytes(a.r * a.tokens);
+    const int tbytes = table_bytes(a.table * a.tokens);
     float *red = reinterpret_cast<float *>(fix_p + (size_t)a.stages * tbytes);
     const uint32_t full = smem_u32(red + 8 * kSlots), empty = full + 8u * a.stages;
     // Tokens are taken `tokens` at a time: batch n holds tokens n * tokens ...
@@ -331,28 +337,46 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
         }
     }
     for (int i = gt; i < 8 * kSlots; i += gthreads) red[i] = 0.f;
-    const int chunks0 = a.job[0].row_bytes / CB, chunks = a.x_bytes / CB;
-    if (threadIdx.x < 4) reinterpret_cast<float *>(smem)[NORM ? chunks * E + threadIdx.x : threadIdx.x] = 0.f;  // zeros
+    // places of the weights' copy: the row's chunks, or the units and one of zeros, which threads
+    // without a unit read
+    const int units0 = a.job[0].nunits, chunks0 = a.job[0].row_bytes / CB;
+    const int places = ORDERED ? units0 + a.job[1].nunits + 1 : a.x_bytes / CB;
+    const uint32_t zero_at = !NORM ? 0u : ORDERED ? (uint32_t)(places - 1) * 16u : (uint32_t)(places * E * 4);
+    auto flipped = [&](int u) { return ORDERED && (u & a.flip) != 0; };
+    if (!ORDERED && threadIdx.x < 4) reinterpret_cast<float *>(smem + zero_at)[threadIdx.x] = 0.f;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if constexpr (NORM) {
         float4 *w = reinterpret_cast<float4 *>(smem);
-        for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-            const bool k = c >= chunks0;
-            const void *src = k ? a.job[1].w : a.job[0].w;
-            const int at = (c - (k ? chunks0 : 0)) * E;
+        for (int i = threadIdx.x; i < (ORDERED ? 2 * places : places); i += blockDim.x) {
+            const int side = ORDERED && i >= places ? 1 : 0, place = i - side * places;
+            const bool k = place >= (ORDERED ? units0 : chunks0);
+            int at = place - (k ? (ORDERED ? units0 : chunks0) : 0);  // the chunk of the row
+            const Rows J = pick(a, k ? 1 : 0);
             float f[E];
-            if (a.w_bf16) load_weights_batched<__nv_bfloat16, E>(static_cast<const __nv_bfloat16 *>(src) + at, f);
-            else load_weights_batched<float, E>(static_cast<const float *>(src) + at, f);
+            if constexpr (ORDERED) {
+                const int u = at, h = u / J.units_per_head, j = u - h * J.units_per_head;
+                const int t = j - a.rot_units, second = t < 0 ? a.rot_units : J.tail_units;  // from first chunk to second
+                const bool pair = t < 0 || t + J.tail_units < J.tail_chunks;
+                at = h * J.head_chunks + (t < 0 ? j : j + a.rot_units) + (pair && (side ^ (flipped(u) ? 1 : 0)) ? second : 0);
+                if (place == places - 1 || (side && !pair)) at = -1;
+            }
 #pragma unroll
-            for (int q = 0; q < E / 4; ++q) w[q * chunks + c] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+            for (int e = 0; e < E; ++e) f[e] = 0.f;
+            if (at >= 0) {
+                if (a.w_bf16) load_weights_batched<__nv_bfloat16, E>(static_cast<const __nv_bfloat16 *>(J.w) + at * E, f);
+                else load_weights_batched<float, E>(static_cast<const float *>(J.w) + at * E, f);
+            }
+#pragma unroll
+            for (int q = 0; q < E / 4; ++q)
+                w[(side * (E / 4) + q) * places + place] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
         }
     }
     __syncthreads();
 
     float2 da[UPT][H], db[UPT][H];  // gradients of the weights, over this group's tokens
     int off_a[UPT], off_b[UPT], tab[UPT];  // stage offsets of a unit's chunks (-1: none), table offset (-1: not turned)
-    uint32_t is_k = 0;
+    uint32_t is_k = 0, flips = 0;  // bit i: unit i is of the keys, has its chunks in the other order
 
     if (gw == a.warps) {
         // ---------------------------------------------------------------- producer warp
@@ -374,6 +398,13 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
             return a.pos64 ? __ldg(static_cast<const long long *>(a.pos) + n)
                            : (int64_t)__ldg(static_cast<const int *>(a.pos) + n);
         };
+        auto entry = [&](float *t, int64_t pt, double turns) {
+            float c, s;
+            cos_sin(pt, turns, a.mscale, a.sign, c, s);
+            t[0] = c;
+            t[nf] = s;
+            if (ORDERED && HALF && a.flip) t[2 * nf] = -s;
+        };
         int stage = 0;
         uint32_t phase = 0;
         bool first = true;  // the first round of stages is filled already
@@ -392,18 +423,15 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
                 for (int i0 = 0; i0 < per * nf; i0 += 32) {
                     const int i = i0 + lane, tok = min(i / nf, per - 1), f = i - i / nf * nf;
                     const int64_t pt = __shfl_sync(0xffffffffu, p, tok);
-                    float *tt = t + tok * a.r;
-                    if (i < per * nf)
-                        cos_sin(pt, __ldg(a.freq + f) * kInvTwoPi, a.mscale, a.sign, tt[place(f)], tt[nf + place(f)]);
+                    if (i < per * nf) entry(t + tok * a.table + place(f), pt, __ldg(a.freq + f) * kInvTwoPi);
                 }
             } else {
-                for (int tok = 0; tok < per; ++tok, t += a.r) {
+                for (int tok = 0; tok < per; ++tok, t += a.table) {
                     const int64_t pt = BATCH ? __shfl_sync(0xffffffffu, p, tok) : p;
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        if (lane + 32 * i < nf) cos_sin(pt, turns[i], a.mscale, a.sign, t[at[i]], t[nf + at[i]]);
-                    for (int f = lane + 64; f < nf; f += 32)
-                        cos_sin(pt, __ldg(a.freq + f) * kInvTwoPi, a.mscale, a.sign, t[place(f)], t[nf + place(f)]);
+                        if (lane + 32 * i < nf) entry(t + at[i], pt, turns[i]);
+                    for (int f = lane + 64; f < nf; f += 32) entry(t + place(f), pt, __ldg(a.freq + f) * kInvTwoPi);
                 }
             }
             p = next;
@@ -426,6 +454,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
     } else {
         // ---------------------------------------------------------------- consumer warps
         const bool wk = !BOTH && gw >= a.warps0;  // a warp of the keys
+        int slot[UPT];  // of the unit's weights
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
             int which = wk ? 1 : 0;
@@ -436,6 +465,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
                 which = 1;
             }
             off_a[i] = off_b[i] = tab[i] = -1;
+            slot[i] = ORDERED ? places - 1 : 0;
             if (which) is_k |= 1u << i;
             if (u >= (which ? a.job[1].nunits : a.job[0].nunits)) continue;
             const Rows J = pick(a, which);
@@ -450,6 +480,13 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
                 off_a[i] = J.row_off + (first + 2 * a.rot_units + t) * CB;
                 if (t + J.tail_units < J.tail_chunks) off_b[i] = off_a[i] + J.tail_units * CB;
             }
+            if constexpr (ORDERED) slot[i] = u + (which ? units0 : 0);
+            if (flipped(u) && off_b[i] >= 0) {
+                const int t = off_a[i];
+                off_a[i] = off_b[i];
+                off_b[i] = t;
+                flips |= 1u << i;
+            }
         }
         if constexpr (BACK) {
 #pragma unroll
@@ -458,15 +495,25 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
                 for (int p = 0; p < H; ++p) da[i][p] = db[i][p] = make_float2(0.f, 0.f);
         }
         const uint32_t sin_off = (uint32_t)a.r * 2u, run = (uint32_t)a.rot_units * H * 4u;  // bytes
-        const uint32_t tables = smem_u32(fix_p), w_s = smem_u32(smem), upper = (uint32_t)chunks * 16u;
+        const uint32_t tables = smem_u32(fix_p), w_s = smem_u32(smem), upper = (uint32_t)places * 16u;
+        // the turns of unit i: flipped, the half layout takes the negative sine, the interleaved one its runs the other way
+        auto load_turns = [&](Turns<H> &cs, uint32_t tab_s, int i) {
+            const bool f = ORDERED && ((flips >> i) & 1u);
+            if constexpr (HALF) cs.load(tab_s + tab[i], run, f ? 2 * sin_off : sin_off);
+            else cs.load(tab_s + tab[i] + (f ? run : 0u), f ? 0u - run : run, sin_off);
+        };
+        auto weights_a = [&](int i) { return w_s + (ORDERED ? (uint32_t)slot[i] * 16u : (uint32_t)max(off_a[i], 0) * (16 / CB)); };
+        auto weights_b = [&](int i) {
+            return w_s + (ORDERED ? (uint32_t)slot[i] * 16u + upper * (uint32_t)(E / 4) : (uint32_t)max(off_b[i], 0) * (16 / CB));
+        };
         // a chunk that is not there reads zeros (behind the weights) and stores nothing
-        const uint32_t zeros = w_s + (NORM ? (uint32_t)(chunks * E * 4) : 0u);
+        const uint32_t zeros = w_s + zero_at;
         // a thread's units lie at the same place of their heads when a head's units divide the
         // warps' stride (powers of two do): cos and sin are then read once per token (not for the
         // gradients, which would spill the registers that keeping them takes)
         bool same = !BACK;
 #pragma unroll
-        for (int i = 1; i < UPT; ++i) same = same && (off_a[i] < 0 || tab[i] == tab[0]);
+        for (int i = 1; i < UPT; ++i) same = same && (off_a[i] < 0 || (tab[i] == tab[0] && ((flips >> i) & 1u) == (flips & 1u)));
         if (!BACK) same = __all_sync(0xffffffffu, same);
         const float d_q = (float)a.job[0].d, d_k = (float)a.job[1].d;
         // rows of the results, moved by the chunk's place in a stage
@@ -483,7 +530,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
         for (int left = first_batch < batches ? (int)((batches - first_batch - 1) / step) + 1 : 0; left > 0; --left) {
             const bool ok = mbar_wait_fast(full + 8u * stage, phase, &g_rotary_error, a.wait_ns);
             const uint32_t src = ring + (uint32_t)(stage * a.stage_bytes + (BATCH ? sub * a.x_bytes : 0));
-            const uint32_t tab_s = tables + (uint32_t)(stage * tbytes + (BATCH ? sub * a.r * 4 : 0));
+            const uint32_t tab_s = tables + (uint32_t)(stage * tbytes + (BATCH ? sub * a.table * 4 : 0));
             const bool live = !BATCH || token < a.T;  // the last batch may have fewer tokens
             float2 va[UPT][H], vb[UPT][H];  // rotary: x; with the norm: x w; gradients: g, dy turned back
             float2 sq[2] = {both(0.f), both(0.f)}, pg[2] = {both(0.f), both(0.f)};  // sums of x^2 and of w g x
@@ -492,7 +539,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
             for (int i = 0; i < UPT; ++i) {
                 const bool has_a = live && off_a[i] >= 0, has_b = live && off_b[i] >= 0;
                 const uint32_t pa = has_a ? src + off_a[i] : zeros, pb = has_b ? src + off_b[i] : zeros;
-                const uint32_t qa = w_s + max(off_a[i], 0) * (16 / CB), qb = w_s + max(off_b[i], 0) * (16 / CB);
+                const uint32_t qa = weights_a(i), qb = weights_b(i);
                 const int m = BOTH ? (is_k >> i) & 1u : 0;
                 if constexpr (MODE == kRotate) {
                     lds_chunk<TA, H>(pa, va[i]);
@@ -517,7 +564,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
                     lds_chunk<TA, H>(has_a ? pa + g_off : zeros, va[i]);
                     lds_chunk<TA, H>(has_b ? pb + g_off : zeros, vb[i]);
                     if (tab[i] >= 0) {
-                        cs.load(tab_s + tab[i], run, sin_off);
+                        load_turns(cs, tab_s, i);
                         turn<H, HALF, false>(va[i], vb[i], cs, 1.f);
                     }
                     float2 q = both(0.f), r = both(0.f), w[H], x[H];
@@ -585,7 +632,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
                 failed = __any_sync(0xffffffffu, failed);
             }
             if (failed) break;
-            if (!BACK && same && tab[0] >= 0) cs.load(tab_s + tab[0], run, sin_off);
+            if (!BACK && same && tab[0] >= 0) load_turns(cs, tab_s, 0);
 #pragma unroll
             for (int i = 0; i < UPT; ++i) {
                 const bool has_a = live && off_a[i] >= 0, has_b = live && off_b[i] >= 0;
@@ -596,7 +643,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
                     const float2 nc = both(-(m ? ck : cq)), inv2 = both(inv);
                     float2 w[H], x[H];
                     lds_chunk<TA, H>(has_a ? src + off_a[i] : zeros, x);
-                    lds_weights<H>(w_s + max(off_a[i], 0) * (16 / CB), upper, w);
+                    lds_weights<H>(weights_a(i), upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) {
                         da[i][p] = __ffma2_rn(va[i][p], __fmul2_rn(x[p], inv2), da[i][p]);
@@ -604,7 +651,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
                     }
                     if (has_a) store_chunk<TA, H>(y + off_a[i], va[i]);
                     lds_chunk<TA, H>(has_b ? src + off_b[i] : zeros, x);
-                    lds_weights<H>(w_s + max(off_b[i], 0) * (16 / CB), upper, w);
+                    lds_weights<H>(weights_b(i), upper, w);
 #pragma unroll
                     for (int p = 0; p < H; ++p) {
                         db[i][p] = __ffma2_rn(vb[i][p], __fmul2_rn(x[p], inv2), db[i][p]);
@@ -613,7 +660,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
                     if (has_b) store_chunk<TA, H>(y + off_b[i], vb[i]);
                 } else {
                     if (tab[i] >= 0) {
-                        if (!same) cs.load(tab_s + tab[i], run, sin_off);
+                        if (!same) load_turns(cs, tab_s, i);
                         turn<H, HALF, NORM>(va[i], vb[i], cs, inv);
                     } else if (NORM) {
 #pragma unroll
@@ -689,8 +736,7 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
 struct Plan {
     bool fits;
     int upt, warps, warps0, groups, threads, tokens;
-    bool mixed;
-
+    bool mixed, ordered;
 };
 
 // Whether the unit kernel takes the call, and its geometry: a rule on the
@@ -757,9 +803,9 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
     return r;
 }
 
-template <typename TA, int E, int MODE, int UPT, bool HALF, int SHAPE>
+template <typename TA, int E, int MODE, int UPT, bool HALF, int SHAPE, bool ORDERED>
 qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bool *taken) {
-    const auto kernel = rotary_unit_kernel<TA, E, MODE, UPT, HALF, SHAPE>;
+    const auto kernel = rotary_unit_kernel<TA, E, MODE, UPT, HALF, SHAPE, ORDERED>;
     static std::atomic<bool> attr_set[64];
     int dev = 0;
     cudaGetDevice(&dev);
@@ -771,7 +817,7 @@ qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bo
     }
     int smem = 0;
     for (p.stages = 8; p.stages >= 1; --p.stages) {
-        smem = p.w_bytes + p.groups * (p.stages * p.stage_bytes + group_fixed(p.r * p.tokens, p.stages));
+        smem = p.w_bytes + p.groups * (p.stages * p.stage_bytes + group_fixed(p.table * p.tokens, p.stages));
         if (smem <= kSmemLimit) break;
     }
     *taken = p.stages >= 1;
@@ -793,17 +839,53 @@ qkn_status launch_kernel(Params &p, const Plan &r, int *grid, cudaStream_t s, bo
     return check_launch("rotary_unit_kernel launch");
 }
 
+template <typename TA, int E, int MODE, int UPT, int SHAPE, bool ORDERED>
+qkn_status launch_ordered(Params &p, const Plan &r, int layout, int *grid, cudaStream_t s, bool *taken) {
+    return layout == QKN_ROTARY_HALF ? launch_kernel<TA, E, MODE, UPT, true, SHAPE, ORDERED>(p, r, grid, s, taken)
+                                     : launch_kernel<TA, E, MODE, UPT, false, SHAPE, ORDERED>(p, r, grid, s, taken);
+}
 template <typename TA, int E, int MODE, int UPT, int SHAPE>
 qkn_status launch_layout(Params &p, const Plan &r, int layout, int *grid, cudaStream_t s, bool *taken) {
-    return layout == QKN_ROTARY_HALF ? launch_kernel<TA, E, MODE, UPT, true, SHAPE>(p, r, grid, s, taken)
-                                     : launch_kernel<TA, E, MODE, UPT, false, SHAPE>(p, r, grid, s, taken);
+    if constexpr (MODE != kRotate)
+        if (r.ordered) return launch_ordered<TA, E, MODE, UPT, SHAPE, true>(p, r, layout, grid, s, taken);
+    return launch_ordered<TA, E, MODE, UPT, SHAPE, false>(p, r, layout, grid, s, taken);
+}
+
+// Whether units next to one another meet in shared memory's banks; sets p.flip.
+//
+// The threads that are served at once (eight with 16 bytes each, sixteen with 8) read without
+// conflict where their chunks differ mod their number.  With units in a head that are not a
+// multiple of it (heads of 64, 80 or 96 bf16, half of 128 turned) the first chunks of all units do
+// not: then the weights lie in the order of the units, and where a power of two of units leaves the
+// first chunks in half of the banks, every other four (eight) units take their second chunk first.
+// 32768 x (4096 + 1024) bf16, norm and gradients: heads of 64 137 -> 114 and 241 -> 193 us, of 96
+// 142 -> 125 and 237 -> 206; heads of 128 lose (108 -> 109, 188 -> 194).  Rotary alone, which reads
+// a chunk once, runs at the copy's rate without.
+template <int CB>
+bool ordered_of(Params &p) {
+    constexpr int L = 128 / CB;
+    const Rows &J = p.job[0];
+    p.flip = 0;
+    if (J.nunits <= L) return false;
+    int seen[2] = {0, 0};
+    for (int u = 0, h = 0, j = 0; u < L; ++u) {
+        const bool turned = j < p.rot_units;
+        const int a = h * J.head_chunks + (turned ? j : j + p.rot_units), b = a + (turned ? p.rot_units : J.tail_units);
+        seen[0] |= 1 << a % L;
+        seen[1] |= 1 << ((u & L / 2) ? b : a) % L;
+        if (++j == J.units_per_head) j = 0, ++h;
+    }
+    const int plain = __builtin_popcount(seen[0]);
+    // (units in no power of two: the pattern changes from head to head)
+    if ((J.units_per_head & (J.units_per_head - 1)) == 0 && __builtin_popcount(seen[1]) > plain) p.flip = L / 2;
+    return plain < L;
 }
 
 // Launches the unit kernel when it takes the call (*taken); *grid is its number of blocks.
 template <typename TA, typename TW, int E, int MODE>
 qkn_status launch_chunks(const Args &a, bool *taken, int *grid, cudaStream_t s) {
     Params p{};
-    const Plan r = plan<TA, E, MODE>(a, p, sizeof(TW));
+    Plan r = plan<TA, E, MODE>(a, p, sizeof(TW));
     *taken = r.fits;
     if (!r.fits) return QKN_OK;
     p.njobs = a.njobs;
@@ -823,7 +905,11 @@ qkn_status launch_chunks(const Args &a, bool *taken, int *grid, cudaStream_t s) 
     p.lanes = 32 / r.tokens;
     p.wait_ns = kWaitTimeoutNs;
     p.w_bf16 = sizeof(TW) == 2;
-    p.w_bytes = (MODE == kRotate ? 0 : (p.job[0].d + p.job[1].d) * 4) + 16;  // 16 bytes of zeros
+    r.ordered = MODE != kRotate && ordered_of<E * (int)sizeof(TA)>(p);
+    p.table = a.r + (p.flip && a.layout == QKN_ROTARY_HALF ? a.r / 2 : 0);
+    // the weights and 16 bytes of zeros
+    p.w_bytes = MODE == kRotate ? 16 : r.ordered ? (p.job[0].nunits + p.job[1].nunits + 1) * 2 * E * 4
+                                                 : (p.job[0].d + p.job[1].d) * 4 + 16;
     constexpr int kUsual = 16 / E;
     if (r.tokens > 1) return launch_layout<TA, E, MODE, kUsual, MULTI>(p, r, a.layout, grid, s, taken);
     if constexpr (MODE == kRotate) {
