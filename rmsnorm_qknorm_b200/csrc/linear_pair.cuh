@@ -2,7 +2,7 @@
 //
 // Included by linear.cu only (one translation unit: its device error word).
 //
-//   C[m][n] = sum_k A(m, k) B(n, k),  256 x 256 (or 128) tiles of C, bf16 in, fp32
+//   C[m][n] = sum_k A(m, k) B(n, k),  256 x 256 (192, 128) tiles of C, bf16 in, fp32
 // accumulated in tensor memory by tcgen05.mma.cta_group::2.  An operand is
 // K-major (rows of consecutive k: x and W of the forward product) or MN-major
 // (consecutive m or n: W in dx = dz W, dz and x in dW = dz^T x), read where it
@@ -13,7 +13,7 @@
 // Roles per CTA (320 threads): warp 0 moves tiles with TMA, one lane of the
 // even CTA's warp 1 issues the MMAs, warps 2-9 run the epilogue of a tile
 // while the MMAs of the next one run into the other accumulator: a quarter of
-// the rows and half of the columns per warp, a row per thread: accumulator
+// the rows and every other 64 columns per warp, a row per thread: accumulator
 // -> times the row's scale, plus bias -> z (stored where asked) -> activation
 // -> plus residual -> y.  y leaves through 32 x 64 boxes in shared memory and
 // TMA stores; the residual comes by TMA into the box that y then overwrites
@@ -36,17 +36,17 @@ constexpr int BAR_BYTES = 320;
 
 constexpr int BOX_COLS = 64, BOX_BYTES = 32 * BOX_COLS * 2;  // an epilogue warp's staging box: 32 rows
 
-// The tile's columns: 256, or 128 where the wider tiles leave pairs without work.
+// The tile's columns: 256, or 192 or 128 where wider tiles leave pairs without work.
 template <int BN> struct Shape {
     static constexpr int EPI_BYTES = EPI_WARPS * 2 * BOX_BYTES;
     static constexpr int BN_CTA = BN / 2;          // rows of B that each CTA loads
     static constexpr int B_BYTES = BN_CTA * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int BIAS_BYTES = BN * 4;
+    static constexpr int BIAS_BYTES = 4 * BOX_COLS * 4;
     static constexpr int STAGES = (227 * 1024 - BAR_BYTES - 1024 - EPI_BYTES - BIAS_BYTES) / STAGE_BYTES;
     static constexpr int PAIR_STAGE_BYTES = 2 * STAGE_BYTES;
-    static constexpr int TMEM_COLS = 2 * BN;       // two accumulators
-    static constexpr int BOXES = BN / 2 / BOX_COLS;  // of an epilogue warp, per tile
+    static constexpr int TMEM_COLS = BN > 128 ? 512 : 256;  // two accumulators
+    static constexpr int BOXES = BN / BOX_COLS;    // of a row of the tile
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + BIAS_BYTES + BAR_BYTES + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024 && (2 * STAGES + 6 + 2 * EPI_WARPS) * 8 <= BAR_BYTES, "shared memory budget");
 };
@@ -215,7 +215,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
                 const uint32_t acc_phase = (it >> 1) & 1;
                 if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&acc_empty[acc]), acc_phase ^ 1u, &g_linear_error))) break;
                 gemm::tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * BN;
+                const uint32_t d_tmem = tmem_base + acc * (S::TMEM_COLS / 2);
                 for (int kb = 0; kb < g.k_blocks; ++kb) {
                     if (!warp_wait(smem_u32(&full[stage]), phase, &g_linear_error)) { ok = false; break; }
                     gemm::tc_fence_after();
@@ -241,11 +241,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     } else {
         // ---------------------------------------------------------------- epilogue (warps 2..9, both CTAs)
         const int quarter = warp & 3;       // TMEM lanes this warp may access: 32 * quarter ...
-        const int half = (warp - 2) >> 2;   // its half of the columns
+        const int half = (warp - 2) >> 2;   // its boxes of the tile: half, half + 2
+        const int own = (S::BOXES + 1 - half) / 2;
         const uint32_t acc_empty_leader0 = map_to_rank(smem_u32(&acc_empty[0]), 0);
         const uint32_t boxes = smem_u32(smem + STAGES * STAGE_BYTES) + (uint32_t)(warp - 2) * 2u * BOX_BYTES;
         const uint32_t rbar = smem_u32(&res_full[2 * (warp - 2)]);
-        float *bias = reinterpret_cast<float *>(smem + STAGES * STAGE_BYTES + S::EPI_BYTES) + half * (BN / 2);
+        float *bias = reinterpret_cast<float *>(smem + STAGES * STAGE_BYTES + S::EPI_BYTES) + half * 2 * BOX_COLS;
         const bool wide = g.wide != 0, has_res = g.has_res != 0;
         uint32_t box = 0, asked = 0;  // boxes stored so far, residual boxes asked for
         bool ok = true;
@@ -254,7 +255,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             int pm, n;
             tile_coords(tile, g, pm, n);
             row0 = pm * 2 * BM + (int)rank * BM + quarter * 32;
-            col0 = n * BN + half * (BN / 2) + j * BOX_COLS;
+            col0 = n * BN + (half + 2 * j) * BOX_COLS;
             return row0 < g.M && col0 < g.N;
         };
         // the residual of a box into the buffer its y leaves from; the stores issued so far have
@@ -278,10 +279,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             const int row = row0 + lane;
             const bool in = row < g.M;
             __nv_bfloat16 *z = g.z != nullptr && in ? g.z + row * g.ldz : nullptr;
-            // the columns' bias: a value per thread of the half's four warps, which share it
+            // the columns' bias, which the four warps of these boxes share
             asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
-            for (int i = quarter * 32 + lane; i < BN / 2; i += 128) {
-                const int c = col0 + i;
+            if (const int i = quarter * 32 + lane; i < own * BOX_COLS) {
+                const int c = col0 + i + (i >= BOX_COLS ? BOX_COLS : 0);
                 float b = 0.f;
                 if (g.epi.bias != nullptr && c < g.N)
                     b = g.epi.bias_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(g.epi.bias)[c])
@@ -292,9 +293,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
             if (ok) ok = warp_wait(smem_u32(&acc_full[acc]), acc_phase, &g_linear_error, product_timeout(g.k_blocks));
             gemm::tc_fence_after();
-            const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN + half * (BN / 2);
-            for (int j = 0; ok && j < S::BOXES; ++j) {
-                const int col = col0 + j * BOX_COLS;
+            const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * (S::TMEM_COLS / 2) + half * BOX_COLS;
+            for (int j = 0; ok && j < own; ++j) {
+                const int col = col0 + 2 * j * BOX_COLS;
                 if (row0 >= g.M || col >= g.N) break;  // the boxes behind it lie outside, too
                 const uint32_t buf = boxes + (box & 1u) * BOX_BYTES;
                 if (has_res) {
@@ -307,7 +308,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
 #pragma unroll 1
                 for (int c = 0; c < BOX_COLS / 32; ++c) {
                     uint32_t v[32];
-                    gemm::tmem_ld_32cols(tbase + j * BOX_COLS + c * 32, v);
+                    gemm::tmem_ld_32cols(tbase + 2 * j * BOX_COLS + c * 32, v);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float2 f[8];
@@ -345,7 +346,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
                     }
                     if (has_res && c == 0) {  // the next box's residual, into the other buffer
                         int r1, c1;
-                        const bool more = j + 1 < S::BOXES && col + BOX_COLS < g.N;
+                        const bool more = j + 1 < own && col + 2 * BOX_COLS < g.N;
                         if (more ? corner(tile, j + 1, r1, c1) : tile + num_pairs < g.num_tiles && corner(tile + num_pairs, 0, r1, c1))
                             fetch(r1, c1);
                     }
@@ -436,17 +437,28 @@ qkn_status launch_bn(const Matrix &a, const Matrix &b, const Matrix &y, const Ma
 }
 
 // About how long the kernel takes, in ns: 4 us, and for every round of tiles over the pairs its
-// products (64 k: 340 ns at 256 columns, 240 ns at 128) or, for short K, its epilogue, which an
-// activation, a residual or a kept z makes longer (`plain` without them).  Measured with 512 ..
-// 12288 columns, K 512 .. 12288 and 128 .. 2048 rows, gelu and a residual: within a tenth of it,
-// e.g. 512 x 4096 x 4096 27.6 us (256 columns, 32 of 74 pairs) against 20.7 (128), 2048 x 4096 x
-// 4096 52.8 against 70.2; without them 4096 x 4096 x 64 15.6.
+// products (64 k: 340 ns at 256 columns, 290 at 192, 240 at 128) or, for short K, its epilogue,
+// which an activation, a residual or a kept z makes longer (`plain` without them).  Measured with
+// 512 .. 12288 columns, K 512 .. 12288 and 128 .. 2048 rows, gelu and a residual: within a tenth of
+// it, e.g. 512 x 4096 x 4096 27.6 us (256 columns, 32 of 74 pairs) against 20.7 (128), 2048 x 4096 x
+// 4096 52.8 against 70.2; without them 4096 x 4096 x 64 15.6; 192 columns against the better of the
+// others: 512 x 12288 x 4096 47 and 57, 1536 x 4096 x 12288 120 and 137.
 inline int64_t cost(int64_t M, int64_t N, int64_t K, int bn, bool plain) {
     const int64_t pairs = sm_count() > 1 ? sm_count() / 2 : 1, kb = (K + BK - 1) / BK;
     const int64_t tiles = ((M + 2 * BM - 1) / (2 * BM)) * ((N + bn - 1) / bn);
-    const int64_t round = bn == 256 ? std::max<int64_t>(plain ? 3000 : 7000, 2500 + 340 * kb)
-                                    : std::max<int64_t>(plain ? 2000 : 4400, 1500 + 240 * kb);
+    const int64_t round = bn == 256   ? std::max<int64_t>(plain ? 3000 : 7000, 2500 + 340 * kb)
+                          : bn == 192 ? std::max<int64_t>(plain ? 3000 : 7000, 2500 + 290 * kb)
+                                      : std::max<int64_t>(plain ? 2000 : 4400, 1500 + 240 * kb);
     return 4000 + (tiles + pairs - 1) / pairs * round;
+}
+
+// The columns of the tile.  MN-major operands come in blocks of 64, of which each CTA takes half a
+// tile's: 256 or 128.
+inline int columns_of(int64_t M, int64_t N, int64_t K, bool k_major, bool plain) {
+    int best = 256;
+    if (k_major && cost(M, N, K, 192, plain) < cost(M, N, K, best, plain)) best = 192;
+    if (cost(M, N, K, 128, plain) < cost(M, N, K, best, plain)) best = 128;
+    return best;
 }
 
 template <bool A_MN, bool B_MN, int ACT>
@@ -461,8 +473,11 @@ qkn_status launch(const Matrix &a, const Matrix &b, const Matrix &y, const Matri
     g.M = (int)y.rows;
     g.N = (int)y.inner;
     const bool plain = ACT == QKN_ACT_NONE && res == nullptr && z == nullptr;
-    const bool narrow = cost(g.M, g.N, K, 128, plain) < cost(g.M, g.N, K, 256, plain);
-    return narrow ? launch_bn<A_MN, B_MN, 128, ACT>(a, b, y, res, g, K, s) : launch_bn<A_MN, B_MN, 256, ACT>(a, b, y, res, g, K, s);
+    const int bn = columns_of(g.M, g.N, K, !A_MN && !B_MN, plain);
+    if constexpr (!A_MN && !B_MN)
+        if (bn == 192) return launch_bn<A_MN, B_MN, 192, ACT>(a, b, y, res, g, K, s);
+    if (bn == 128) return launch_bn<A_MN, B_MN, 128, ACT>(a, b, y, res, g, K, s);
+    return launch_bn<A_MN, B_MN, 256, ACT>(a, b, y, res, g, K, s);
 }
 
 }  // namespace pair

@@ -324,7 +324,7 @@ inline int tokens_per_tile(int64_t M, int64_t N, int64_t K, bool forward, bool p
     for (int bt = 2 * least; bt <= 128; bt *= 2)
         if (cost(M, N, K, bt) < cost(M, N, K, best)) best = bt;
     if ((M + best - 1) / best > 65535) return 0;  // the grid's second dimension
-    if (!(forward && M <= 64) && cost(M, N, K, best) >= std::min(pair::cost(M, N, K, 128, plain), pair::cost(M, N, K, 256, plain))) return 0;
+    if (!(forward && M <= 64) && cost(M, N, K, best) >= pair::cost(M, N, K, pair::columns_of(M, N, K, forward, plain), plain)) return 0;
     return best;
 }
 

@@ -91,10 +91,12 @@ SIZES = [(1, 64, 64), (1, 264, 1000), (2, 8, 8), (3, 128, 72), (17, 520, 136), (
          (1500, 4104, 1600)]
 # One for each kernel and tile that the sizes choose between on 148 SMs: of the forward product the
 # kernel for few rows with 32, 64 and 128 tokens per tile, then the pair kernel with 128 and 256
-# columns (16 tokens are taken by the small ones above); the same of dx; of dW.
+# columns (16 tokens are taken by the small ones above); the same of dx; of dW; the forward product
+# with 192 columns.
 SIZES += [(65, 3728, 8), (333, 2704, 8), (500, 3464, 8), (333, 3344, 264), (1000, 3464, 72),
           (65, 8, 3736), (500, 8, 1696), (65, 712, 3080), (333, 264, 3336), (1000, 72, 3816),
-          (100, 8, 8), (1000, 3224, 8), (200, 3272, 264), (65, 3528, 912)]
+          (100, 8, 8), (1000, 3224, 8), (200, 3272, 264), (65, 3528, 912),
+          (257, 4848, 1000)]
 
 
 @pytest.mark.parametrize("act", ACTS)
