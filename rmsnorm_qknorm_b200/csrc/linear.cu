@@ -2,8 +2,9 @@
 //
 //   z = r_m sum_k x[m][k] W[n][k] + b[n],  y = act(z) + residual
 //   dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum_m dz
-// The products run on the tensor cores (linear_pair.cuh) with everything else
-// in their epilogue; dz is formed once (and rounded to bf16, the products'
+// The products run on the tensor cores (linear_rows.cuh for few rows,
+// linear_pair.cuh for many, linear_split.cuh between) with everything else in
+// their epilogue; dz is formed once (and rounded to bf16, the products'
 // operand type) by an element-wise pass that adds up db in fp32 on the way.
 #include <algorithm>
 #include <atomic>
@@ -24,6 +25,7 @@ __device__ int g_linear_error = 0;
 
 #include "linear_pair.cuh"
 #include "linear_rows.cuh"
+#include "linear_split.cuh"
 
 namespace lin {
 
@@ -133,12 +135,23 @@ qkn_status launch_dz(const __nv_bfloat16 *dy, const __nv_bfloat16 *z, __nv_bfloa
     return check_launch("linear_dz_kernel launch");
 }
 
-template <int ACT>
-qkn_status forward(const pair::Matrix &x, const pair::Matrix &W, const pair::Matrix &y, const pair::Matrix *res,
+// One product by the kernel with the least estimated time.  Forward: x [M][K], W [N][K].  dx: dz and
+// W (MN-major), dW: dz and x (both MN-major).
+template <bool A_MN, bool B_MN, int ACT>
+qkn_status product(const pair::Matrix &a, const pair::Matrix &b, const pair::Matrix &y, const pair::Matrix *res,
                    const pair::Matrix *z, const Epilogue &epi, int64_t K, cudaStream_t s) {
-    if (const int tokens = rows::tokens_per_tile(y.rows, y.inner, K, true, ACT == QKN_ACT_NONE && !res && !z, 16))
-        return rows::launch<ACT, false, false>(x, W, y, res, z, epi, K, tokens, s);
-    return pair::launch<false, false, ACT>(x, W, y, res, z, epi, K, s);
+    constexpr bool kForward = !A_MN && !B_MN;
+    const bool plain = ACT == QKN_ACT_NONE && !res && !z;
+    const int64_t M = y.rows, N = y.inner;
+    const int tokens = rows::tokens_per_tile(M, N, K, kForward, plain, A_MN ? 64 : 16);
+    if (M > 64) {
+        const int64_t others = tokens ? rows::cost(M, N, K, tokens)
+                                      : pair::cost(M, N, K, pair::columns_of(M, N, K, kForward, plain), plain);
+        if (const split::Choice c = split::choose(M, N, K, others); c.columns)
+            return split::launch<A_MN, B_MN, ACT>(a, b, y, res, z, epi, K, c, s);
+    }
+    if (tokens) return rows::launch<ACT, B_MN, A_MN>(a, b, y, res, z, epi, K, tokens, s);
+    return pair::launch<A_MN, B_MN, ACT>(a, b, y, res, z, epi, K, s);
 }
 
 bool pitch_ok(int64_t ld, int64_t width) { return ld >= width && ld % 8 == 0; }
@@ -200,11 +213,11 @@ extern "C" QKN_API qkn_status linear_fused(const void *x, const void *W, void *y
     e.bias = bias;
     e.bias_bf16 = bias_dt == QKN_BF16;
     switch (act) {
-    case QKN_ACT_RELU: return lin::forward<QKN_ACT_RELU>(mx, mw, my, res, z, e, K, s);
-    case QKN_ACT_SILU: return lin::forward<QKN_ACT_SILU>(mx, mw, my, res, z, e, K, s);
-    case QKN_ACT_GELU: return lin::forward<QKN_ACT_GELU>(mx, mw, my, res, z, e, K, s);
-    case QKN_ACT_GELU_TANH: return lin::forward<QKN_ACT_GELU_TANH>(mx, mw, my, res, z, e, K, s);
-    default: return lin::forward<QKN_ACT_NONE>(mx, mw, my, res, z, e, K, s);
+    case QKN_ACT_RELU: return lin::product<false, false, QKN_ACT_RELU>(mx, mw, my, res, z, e, K, s);
+    case QKN_ACT_SILU: return lin::product<false, false, QKN_ACT_SILU>(mx, mw, my, res, z, e, K, s);
+    case QKN_ACT_GELU: return lin::product<false, false, QKN_ACT_GELU>(mx, mw, my, res, z, e, K, s);
+    case QKN_ACT_GELU_TANH: return lin::product<false, false, QKN_ACT_GELU_TANH>(mx, mw, my, res, z, e, K, s);
+    default: return lin::product<false, false, QKN_ACT_NONE>(mx, mw, my, res, z, e, K, s);
     }
 }
 
@@ -297,15 +310,11 @@ extern "C" QKN_API qkn_status linear_fused_backward(const void *dy, const void *
     const lin::Epilogue e{};
     if (st == QKN_OK && dx != nullptr) {
         const lin::pair::Matrix out = {dx, M, K, lddx};
-        const int tokens = lin::rows::tokens_per_tile(M, K, N, false, true, 16);
-        st = tokens ? lin::rows::launch<QKN_ACT_NONE, true, false>(mg, mw, out, nullptr, nullptr, e, N, tokens, s)
-                    : lin::pair::launch<false, true, QKN_ACT_NONE>(mg, mw, out, nullptr, nullptr, e, N, s);
+        st = lin::product<false, true, QKN_ACT_NONE>(mg, mw, out, nullptr, nullptr, e, N, s);
     }
     if (st == QKN_OK && dW != nullptr) {
         const lin::pair::Matrix out = {dW, N, K, lddw};
-        const int tokens = lin::rows::tokens_per_tile(N, K, M, false, true, 64);
-        st = tokens ? lin::rows::launch<QKN_ACT_NONE, true, true>(mg, mx, out, nullptr, nullptr, e, M, tokens, s)
-                    : lin::pair::launch<true, true, QKN_ACT_NONE>(mg, mx, out, nullptr, nullptr, e, M, s);
+        st = lin::product<true, true, QKN_ACT_NONE>(mg, mx, out, nullptr, nullptr, e, M, s);
     }
     if (own != nullptr) {
         const cudaError_t f = cudaFreeAsync(own, s);

@@ -79,14 +79,23 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     return v;
 }
 
-// Adds up the partials of this CTA's tokens and runs the epilogue: a warp per
-// token, four features per thread, TOKENS tokens at a time.
-template <int ACT, int MAX_RANKS, int TOKENS, int BT>
-__device__ __forceinline__ void finish(const Args &g, uint32_t tile, const float (&bias)[4], int n0, int t0, int rank,
-                                       int ranks) {
-    constexpr int kStep = THREADS / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int valid = min(BT, g.M - t0), n = n0 + 4 * lane;
+// The bias of features n .. n + 3 (zero where there is none).
+__device__ __forceinline__ void load_bias(const Args &g, int n, float (&bias)[4]) {
+    bias[0] = bias[1] = bias[2] = bias[3] = 0.f;
+    if (g.epi.bias == nullptr || n >= g.N) return;
+    if (g.epi.bias_bf16) load_weights_batched<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(g.epi.bias) + n, bias);
+    else load_weights_batched<float, 4>(static_cast<const float *>(g.epi.bias) + n, bias);
+}
+
+// Adds up the partials of a CTA's tokens (rank, rank + ranks, ... of the tile's
+// `valid`) and runs the epilogue: a warp of the block's NTHREADS per token, the
+// features n .. n + 3 per thread, TOKENS tokens at a time.  partial(t, s) is
+// the cluster address of token t's four features in rank s.
+template <int ACT, int MAX_RANKS, int TOKENS, int NTHREADS, typename Partial>
+__device__ __forceinline__ void finish(const Args &g, const Partial &partial, const float (&bias)[4], int n, int t0,
+                                       int valid, int rank, int ranks) {
+    constexpr int kStep = NTHREADS / 32;
+    const int warp = threadIdx.x >> 5;
     if (n >= g.N) return;  // N is a multiple of 8
     for (int i = warp; rank + i * ranks < valid; i += TOKENS * kStep) {
         float4 part[TOKENS][MAX_RANKS];
@@ -98,7 +107,7 @@ __device__ __forceinline__ void finish(const Args &g, uint32_t tile, const float
             if (t >= valid) continue;
 #pragma unroll
             for (int s = 0; s < MAX_RANKS; ++s)
-                if (s < ranks) part[u][s] = ld_cluster_f32x4(map_to_rank(tile + (uint32_t)(t * BF + 4 * lane) * 4u, (uint32_t)s));
+                if (s < ranks) part[u][s] = ld_cluster_f32x4(partial(t, s));
             if (g.res != nullptr) q[u] = *reinterpret_cast<const uint2 *>(g.res + (int64_t)(t0 + t) * g.ldr + n);  // may be y itself
         }
 #pragma unroll
@@ -216,11 +225,8 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
         elect_commit<1>(smem_u32(acc_full));  // every MMA issued here has completed
         __syncwarp();
     }
-    float bias[4] = {0.f, 0.f, 0.f, 0.f};  // of this thread's four features in the last step
-    if (g.epi.bias != nullptr && n0 + 4 * lane < g.N) {
-        if (g.epi.bias_bf16) load_weights_batched<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(g.epi.bias) + n0 + 4 * lane, bias);
-        else load_weights_batched<float, 4>(static_cast<const float *>(g.epi.bias) + n0 + 4 * lane, bias);
-    }
+    float bias[4];  // of this thread's four features in the last step
+    load_bias(g, n0 + 4 * lane, bias);
     // every thread: the accumulator is complete and no MMA reads the ring any more
     mbar_wait(smem_u32(acc_full), 0u, &g_linear_error, product_timeout(kb1 - kb0));
     gemm::tc_fence_after();
@@ -242,9 +248,11 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
     // Tokens rank, rank + ranks, ... of the tile: up to 16 partials of a thread's four features
     // are asked for before the first is added
     const uint32_t at = smem_u32(tile);
-    if (ranks <= 2) finish<ACT, 2, 8, BT>(g, at, bias, n0, t0, rank, ranks);
-    else if (ranks <= 4) finish<ACT, 4, 4, BT>(g, at, bias, n0, t0, rank, ranks);
-    else finish<ACT, kMaxCluster, 2, BT>(g, at, bias, n0, t0, rank, ranks);
+    const int n = n0 + 4 * lane, valid = min(BT, g.M - t0);
+    auto partial = [&](int t, int s) { return map_to_rank(at + (uint32_t)(t * BF + 4 * lane) * 4u, (uint32_t)s); };
+    if (ranks <= 2) finish<ACT, 2, 8, THREADS>(g, partial, bias, n, t0, valid, rank, ranks);
+    else if (ranks <= 4) finish<ACT, 4, 4, THREADS>(g, partial, bias, n, t0, valid, rank, ranks);
+    else finish<ACT, kMaxCluster, 2, THREADS>(g, partial, bias, n, t0, valid, rank, ranks);
     if (ranks > 1) cluster_sync();  // the other CTAs have read this one's tile
     else __syncthreads();
     if (warp == 1) {
@@ -316,9 +324,9 @@ inline int64_t cost(int64_t M, int64_t N, int64_t K, int bt) {
 
 // Tokens per tile (`least` or more) for a product of M tokens, N features and K, 0 where the pair
 // kernel is estimated faster.  Forward products of up to 64 rows, where the weights are the
-// traffic, it always serves; e.g. 256 x 4096 x
-// 4096 19.3 us against 20.6 by the pair kernel, 128 x 12288 x 4096 36.7 against 32.1, 1024 x 1024
-// x 1024 9.2 against 9.3, 512 x 4096 x 4096 31.3 against 20.7.
+// traffic, it always serves; e.g. 256 x 4096 x 4096 19.3 us against 20.6 by the pair kernel, 128 x
+// 12288 x 4096 36.7 against 32.1, 1024 x 1024 x 1024 9.2 against 9.3, 512 x 4096 x 4096 31.3 against
+// 20.7.
 inline int tokens_per_tile(int64_t M, int64_t N, int64_t K, bool forward, bool plain, int least) {
     int best = least;
     for (int bt = 2 * least; bt <= 128; bt *= 2)
@@ -328,10 +336,7 @@ inline int tokens_per_tile(int64_t M, int64_t N, int64_t K, bool forward, bool p
     return best;
 }
 
-// y[token][feature] = epilogue of sum_k F(feature, k) T(token, k).
-template <int ACT, bool F_MN, bool T_MN>
-qkn_status launch(const pair::Matrix &t, const pair::Matrix &f, const pair::Matrix &y, const pair::Matrix *res,
-                  const pair::Matrix *z, const Epilogue &epi, int64_t K, int tokens, cudaStream_t s) {
+inline Args args_of(const pair::Matrix &y, const pair::Matrix *res, const pair::Matrix *z, const Epilogue &epi, int64_t K) {
     Args a;
     a.epi = epi;
     a.res = res ? static_cast<const __nv_bfloat16 *>(res->p) : nullptr;
@@ -343,6 +348,14 @@ qkn_status launch(const pair::Matrix &t, const pair::Matrix &f, const pair::Matr
     a.M = (int)y.rows;
     a.N = (int)y.inner;
     a.k_blocks = (int)((K + BK - 1) / BK);
+    return a;
+}
+
+// y[token][feature] = epilogue of sum_k F(feature, k) T(token, k).
+template <int ACT, bool F_MN, bool T_MN>
+qkn_status launch(const pair::Matrix &t, const pair::Matrix &f, const pair::Matrix &y, const pair::Matrix *res,
+                  const pair::Matrix *z, const Epilogue &epi, int64_t K, int tokens, cudaStream_t s) {
+    const Args a = args_of(y, res, z, epi, K);
     if constexpr (!T_MN) {
         if (tokens == 16) return launch_bt<16, ACT, F_MN, false>(t, f, a, s);
         if (tokens == 32) return launch_bt<32, ACT, F_MN, false>(t, f, a, s);

@@ -92,11 +92,14 @@ SIZES = [(1, 64, 64), (1, 264, 1000), (2, 8, 8), (3, 128, 72), (17, 520, 136), (
 # One for each kernel and tile that the sizes choose between on 148 SMs: of the forward product the
 # kernel for few rows with 32, 64 and 128 tokens per tile, then the pair kernel with 128 and 256
 # columns (16 tokens are taken by the small ones above); the same of dx; of dW; the forward product
-# with 192 columns.
+# with 192 columns; split over the pairs of a cluster, 128 columns and 2 and 3 pairs, 256 and 2, 3 and 4, the
+# same of dx and dW.
 SIZES += [(65, 3728, 8), (333, 2704, 8), (500, 3464, 8), (333, 3344, 264), (1000, 3464, 72),
           (65, 8, 3736), (500, 8, 1696), (65, 712, 3080), (333, 264, 3336), (1000, 72, 3816),
           (100, 8, 8), (1000, 3224, 8), (200, 3272, 264), (65, 3528, 912),
-          (257, 4848, 1000)]
+          (257, 4848, 1000), (129, 3736, 1000), (129, 2384, 2312), (65, 6336, 3952),
+          (129, 4776, 1984), (65, 3736, 5264),
+          (520, 800, 1216), (264, 2152, 2096), (136, 2256, 2360), (1001, 1632, 424), (3001, 280, 2096), (3001, 1216, 336)]
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -322,3 +325,26 @@ def test_results_of_columns_beside_the_inputs(cuda_lib):
     assert torch.equal(qk.linear_fused(x, W, out=y), ref)
     with pytest.raises(qk.QKNormError, match="shares memory"):
         qk.linear_fused(x, W, out=buf[:M, 56: 56 + N])
+
+
+@pytest.mark.parametrize("M,N,K", [(129, 3736, 1000), (300, 4096, 8192)])  # split over two pairs, 128 and 256 columns
+def test_split_products_on_views(cuda_lib, M, N, K):
+    x, W, b, res = normal(M, K, seed=1), normal(N, K, seed=2, scale=K ** -0.5), normal(N, seed=3), normal(M, N, seed=4)
+    inv = torch.rand(M, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV) + 0.5
+    z = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    want = qk.linear_fused(x, W, b, "silu", res, inv_rms=inv, preact_out=z)
+    buf = torch.full((M + 2, 2 * N + 48), 7.0, dtype=torch.bfloat16, device=DEV)
+    y, zv = buf[1: M + 1, 8: 8 + N], buf[1: M + 1, N + 24: 2 * N + 24]
+    y.copy_(res)
+    xv = torch.empty(M, K + 8, dtype=torch.bfloat16, device=DEV)[:, :K].copy_(x)
+    for _ in range(3):  # the same bits every time
+        qk.linear_fused(xv, W, b, "silu", y, inv_rms=inv, preact_out=zv, out=y)
+        assert torch.equal(y, want) and torch.equal(zv, z)
+        y.copy_(res)
+    y.fill_(7.0)
+    zv.fill_(7.0)
+    assert bool((buf == 7.0).all())
+    bad = x.clone()
+    bad[M - 2] = float("nan")
+    got = qk.linear_fused(bad, W, b, "silu", res, inv_rms=inv)
+    assert torch.isnan(got[M - 2]).all() and torch.equal(got[:M - 2], want[:M - 2]) and torch.equal(got[M - 1], want[M - 1])
