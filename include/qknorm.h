@@ -436,7 +436,8 @@ QKN_API qkn_status qknorm_rotary(const void *q, const void *k, const void *wq, c
  * q, k, wq, wk                    the forward call's inputs
  * dq_in, dk_in                    results in `act`, pitches lddq, lddk; sharing
  *                                 memory with an input is refused
- * dwq [dq], dwk [dk]              results, fp32, always written (zeros when T == 0)
+ * dwq [dq], dwk [dk]              results, fp32, always written (zeros when T == 0),
+ *                                 apart from the rows and from one another
  * workspace    at least qknorm_rotary_backward_workspace_bytes(T, dq, dk)
  *              bytes of device scratch, 16-byte aligned, or NULL to allocate
  *              it stream-ordered inside the call

@@ -322,7 +322,10 @@ extern "C" QKN_API qkn_status linear_fused_backward(const void *dy, const void *
         bool met = lin::meets(results[0], results[1]);
         for (const lin::pair::Matrix &r : results)
             for (const lin::pair::Matrix &m : inputs) met = met || lin::meets(r, m);
-        if (met) return fail(QKN_ERR_UNSUPPORTED, "%s: dx or dW shares memory with an input or with one another", fn);
+        const lin::pair::Matrix sums = {dbias, 1, 2 * N, 2 * N};  // N floats as bf16
+        for (const lin::pair::Matrix &r : results) met = met || lin::meets(sums, r);
+        for (const lin::pair::Matrix &m : inputs) met = met || lin::meets(sums, m);
+        if (met) return fail(QKN_ERR_UNSUPPORTED, "%s: dx, dW or dbias shares memory with an input or with one another", fn);
     }
     void *own = nullptr;
     if (workspace == nullptr && (has_z || dbias != nullptr)) {

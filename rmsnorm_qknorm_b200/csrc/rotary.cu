@@ -392,6 +392,9 @@ qkn_status check_rotary_rows(const char *fn, const Args &a, int64_t es, bool inp
             if ((rows_overlap(y, x) && !(inplace && o == i && same_rows(y, x))) || rows_overlap(y, g) ||
                 (o > i && rows_overlap(y, z)))
                 return fail(QKN_ERR_UNSUPPORTED, "%s: a result shares memory with an input or the other result", fn);
+            const Span w = {j.dw, 1, 4 * (int64_t)j.d, 0}, v = {k.dw, 1, 4 * (int64_t)k.d, 0};  // of gradients
+            if (rows_overlap(w, x) || rows_overlap(w, g) || rows_overlap(w, z) || (o > i && rows_overlap(w, v)))
+                return fail(QKN_ERR_UNSUPPORTED, "%s: the gradient of weights shares memory with rows or the other's", fn);
         }
     }
     return QKN_OK;

@@ -82,6 +82,7 @@ def test_results_over_inputs_are_refused(lib, kw):
     assert "shares memory" in lib.qkn_last_error().decode()
 
 
-@pytest.mark.parametrize("kw", [dict(dx=P), dict(dx=2 * P, dW=P), dict(dx=2 * P, dW=2 * P), dict(dx=2 * P, dW=2 * P + 256)])
+@pytest.mark.parametrize("kw", [dict(dx=P), dict(dx=2 * P, dW=P), dict(dx=2 * P, dW=2 * P), dict(dx=2 * P, dW=2 * P + 256),
+                                dict(dx=2 * P, dW=4 * P, db=2 * P + 508), dict(dx=2 * P, dW=4 * P, db=P + 4)])
 def test_gradients_over_inputs_are_refused(lib, kw):
     assert back(lib, **kw) == UNSUP

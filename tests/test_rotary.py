@@ -138,3 +138,12 @@ def test_results_over_inputs_are_refused(lib, kw):
 def test_gradients_over_inputs_are_refused(lib):
     for kw in (dict(dqi=P), dict(gq=P, q=4 * P, dqi=4 * P), dict(gq=P, q=4 * P, dqi=P + 512)):
         assert back(lib, **kw) == UNSUP, kw
+
+
+# gq, gk, q, k, dq_in, dk_in lie at P .. 6 P, the weights at 7 P and 8 P
+@pytest.mark.parametrize("dwq,dwk", [(9 * P, 9 * P), (9 * P, 9 * P + 508), (6 * P + 4, 10 * P), (9 * P, P + 1020)])
+def test_weight_gradients_over_others_are_refused(lib, dwq, dwk):
+    assert lib.qknorm_rotary_backward(P, 2 * P, 3 * P, 4 * P, 7 * P, 8 * P, 5 * P, 6 * P, dwq, dwk, 4, 128, 64, 128, 64, 128,
+                                      64, 128, 64, 64, 11 * P, 64, 12 * P, 64, 0, 1.0, BF16, BF16, 1e-6, 13 * P, 1 << 16,
+                                      None) == UNSUP
+    assert "gradient of weights" in lib.qkn_last_error().decode()
