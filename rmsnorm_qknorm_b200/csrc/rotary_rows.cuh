@@ -337,29 +337,30 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
         }
     }
     for (int i = gt; i < 8 * kSlots; i += gthreads) red[i] = 0.f;
-    // places of the weights' copy: the row's chunks, or the units and one of zeros, which threads
-    // without a unit read
+    // places of the weights' copy: the row's chunks or the units, and one of zeros.  What a thread has no
+    // chunk for it reads there, its rows' elements and its weights: 0 times another weight would be
+    // NaN where that weight is not finite
     const int units0 = a.job[0].nunits, chunks0 = a.job[0].row_bytes / CB;
-    const int places = ORDERED ? units0 + a.job[1].nunits + 1 : a.x_bytes / CB;
-    const uint32_t zero_at = !NORM ? 0u : ORDERED ? (uint32_t)(places - 1) * 16u : (uint32_t)(places * E * 4);
+    const int places = (ORDERED ? units0 + a.job[1].nunits : a.x_bytes / CB) + 1;
+    const uint32_t zero_at = NORM ? (uint32_t)(places - 1) * 16u : 0u;
     auto flipped = [&](int u) { return ORDERED && (u & a.flip) != 0; };
-    if (!ORDERED && threadIdx.x < 4) reinterpret_cast<float *>(smem + zero_at)[threadIdx.x] = 0.f;
+    if (!NORM && threadIdx.x < 4) reinterpret_cast<float *>(smem)[threadIdx.x] = 0.f;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if constexpr (NORM) {
         float4 *w = reinterpret_cast<float4 *>(smem);
         for (int i = threadIdx.x; i < (ORDERED ? 2 * places : places); i += blockDim.x) {
             const int side = ORDERED && i >= places ? 1 : 0, place = i - side * places;
-            const bool k = place >= (ORDERED ? units0 : chunks0);
-            int at = place - (k ? (ORDERED ? units0 : chunks0) : 0);  // the chunk of the row
+            const bool k = place >= (ORDERED ? units0 : chunks0), last = place == places - 1;
+            int at = last ? -1 : place - (k ? (ORDERED ? units0 : chunks0) : 0);  // the chunk of the row, -1: zeros
             const Rows J = pick(a, k ? 1 : 0);
             float f[E];
-            if constexpr (ORDERED) {
+            if (ORDERED && !last) {
                 const int u = at, h = u / J.units_per_head, j = u - h * J.units_per_head;
                 const int t = j - a.rot_units, second = t < 0 ? a.rot_units : J.tail_units;  // from first chunk to second
                 const bool pair = t < 0 || t + J.tail_units < J.tail_chunks;
                 at = h * J.head_chunks + (t < 0 ? j : j + a.rot_units) + (pair && (side ^ (flipped(u) ? 1 : 0)) ? second : 0);
-                if (place == places - 1 || (side && !pair)) at = -1;
+                if (side && !pair) at = -1;
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) f[e] = 0.f;
@@ -502,12 +503,11 @@ __global__ void __launch_bounds__(max_threads<MODE, UPT, E>(), 1) rotary_unit_ke
             if constexpr (HALF) cs.load(tab_s + tab[i], run, f ? 2 * sin_off : sin_off);
             else cs.load(tab_s + tab[i] + (f ? run : 0u), f ? 0u - run : run, sin_off);
         };
-        auto weights_a = [&](int i) { return w_s + (ORDERED ? (uint32_t)slot[i] * 16u : (uint32_t)max(off_a[i], 0) * (16 / CB)); };
-        auto weights_b = [&](int i) {
-            return w_s + (ORDERED ? (uint32_t)slot[i] * 16u + upper * (uint32_t)(E / 4) : (uint32_t)max(off_b[i], 0) * (16 / CB));
-        };
         // a chunk that is not there reads zeros (behind the weights) and stores nothing
         const uint32_t zeros = w_s + zero_at;
+        auto weights_at = [&](int off) { return off < 0 ? zeros : w_s + (uint32_t)off * (16 / CB); };
+        auto weights_a = [&](int i) { return ORDERED ? w_s + (uint32_t)slot[i] * 16u : weights_at(off_a[i]); };
+        auto weights_b = [&](int i) { return ORDERED ? w_s + (uint32_t)slot[i] * 16u + upper * (uint32_t)(E / 4) : weights_at(off_b[i]); };
         // a thread's units lie at the same place of their heads when a head's units divide the
         // warps' stride (powers of two do): cos and sin are then read once per token (not for the
         // gradients, which would spill the registers that keeping them takes)
@@ -907,9 +907,9 @@ qkn_status launch_chunks(const Args &a, bool *taken, int *grid, cudaStream_t s) 
     p.w_bf16 = sizeof(TW) == 2;
     r.ordered = MODE != kRotate && ordered_of<E * (int)sizeof(TA)>(p);
     p.table = a.r + (p.flip && a.layout == QKN_ROTARY_HALF ? a.r / 2 : 0);
-    // the weights and 16 bytes of zeros
+    // the weights and a place of zeros
     p.w_bytes = MODE == kRotate ? 16 : r.ordered ? (p.job[0].nunits + p.job[1].nunits + 1) * 2 * E * 4
-                                                 : (p.job[0].d + p.job[1].d) * 4 + 16;
+                                                 : (p.job[0].d + p.job[1].d + E) * 4;
     constexpr int kUsual = 16 / E;
     if (r.tokens > 1) return launch_layout<TA, E, MODE, kUsual, MULTI>(p, r, a.layout, grid, s, taken);
     if constexpr (MODE == kRotate) {
