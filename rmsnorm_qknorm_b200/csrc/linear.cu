@@ -110,7 +110,6 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const __nv_bfloat
         for (int r = 1; r < slices; ++r) s += ld_cluster_f32(map_to_rank(smem_u32(&total[threadIdx.x]), (uint32_t)r));
         db[c] = s;
     }
-    __syncwarp();
     cluster_sync();  // the first block has read this one's sums
 }
 

@@ -308,6 +308,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
 #pragma unroll 1
                 for (int c = 0; c < BOX_COLS / 32; ++c) {
                     uint32_t v[32];
+                    __syncwarp();  // rows behind the last store no z, one lane asks for the residual
                     gemm::tmem_ld_32cols(tbase + 2 * j * BOX_COLS + c * 32, v);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {

@@ -230,6 +230,7 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
     // every thread: the accumulator is complete and no MMA reads the ring any more
     mbar_wait(smem_u32(acc_full), 0u, &g_linear_error, product_timeout(kb1 - kb0));
     gemm::tc_fence_after();
+    __syncwarp();  // lanes come from the bias and the wait; tensor memory is read by whole warps
     __syncthreads();
     float *tile = reinterpret_cast<float *>(smem);  // [BT tokens][BF features]
     if (warp >= 2) {
@@ -253,6 +254,7 @@ linear_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_cons
     if (ranks <= 2) finish<ACT, 2, 8, THREADS>(g, partial, bias, n, t0, valid, rank, ranks);
     else if (ranks <= 4) finish<ACT, 4, 4, THREADS>(g, partial, bias, n, t0, valid, rank, ranks);
     else finish<ACT, kMaxCluster, 2, THREADS>(g, partial, bias, n, t0, valid, rank, ranks);
+    __syncwarp();  // lanes whose features lie behind the last have left `finish` before the others
     if (ranks > 1) cluster_sync();  // the other CTAs have read this one's tile
     else __syncthreads();
     if (warp == 1) {

@@ -124,6 +124,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_con
     // every thread: the accumulator is complete and no MMA reads either CTA's ring any more
     mbar_wait_cluster(smem_u32(acc_full), 0u, &g_linear_error, product_timeout(kb1 - kb0));
     gemm::tc_fence_after();
+    __syncwarp();  // tensor memory is read by whole warps
     __syncthreads();
     // this CTA's rows of the partial tile: [128][BN] fp32, chunk c of row i at c ^ (i & 7)
     const uint32_t mine = smem_u32(smem);

@@ -131,8 +131,11 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
     return r;
 }
 
-// All threads of every CTA of the cluster (a hardware barrier, like __syncthreads).
+// All threads of every CTA of the cluster (a hardware barrier, like __syncthreads).  Its aligned
+// instructions are defined only where the whole warp executes them together; callers come from
+// branches that lanes take apart.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
