@@ -392,10 +392,11 @@ typedef enum {
  *
  * q [T][dq], k [T][dk], pitches ldq, ldk; dk == 0 rotates q only.  q_out ==
  * NULL (resp. k_out == NULL) works in place.  A result that shares
- * memory with an input in any other way, or with the other result, is refused
- * (QKN_ERR_UNSUPPORTED); columns of one wider buffer are fine.  inverse != 0 turns back (the
- * sine's sign is flipped, mscale is still applied): the gradient of the call
- * without it.  fp32 arithmetic, one rounding to `act`.  Any element-aligned
+ * memory with an input in any other way (rows, positions, inv_freq, and with
+ * the norm the weights), or with the other result, is refused
+ * (QKN_ERR_UNSUPPORTED); columns of one wider buffer are fine.  inverse != 0
+ * turns back (the sine's sign is flipped, mscale is still applied): the
+ * gradient of the call without it.  fp32 arithmetic, one rounding to `act`.  Any element-aligned
  * pointers and pitches are accepted; 16-byte aligned rows of whole 16 bytes
  * with head_dim a multiple of 4 and rotary_dim of 8 take the fast kernel.
  */
@@ -437,10 +438,11 @@ QKN_API qkn_status qknorm_rotary(const void *q, const void *k, const void *wq, c
  * dq_in, dk_in                    results in `act`, pitches lddq, lddk; sharing
  *                                 memory with an input is refused
  * dwq [dq], dwk [dk]              results, fp32, always written (zeros when T == 0),
- *                                 apart from the rows and from one another
+ *                                 apart from every input and from one another
  * workspace    at least qknorm_rotary_backward_workspace_bytes(T, dq, dk)
  *              bytes of device scratch, 16-byte aligned, or NULL to allocate
- *              it stream-ordered inside the call
+ *              it stream-ordered inside the call; sharing the bytes that are
+ *              needed with an input or a result is refused
  * Sums are fp32 in a fixed order: repeated calls give the same bits.
  */
 QKN_API qkn_status qknorm_rotary_backward(const void *dq_out, const void *dk_out,
@@ -479,15 +481,16 @@ typedef enum {
  *
  * x         [M][K] bf16, pitch ldx
  * W         [N][K] bf16 (K contiguous), pitch ldw
- * y         [M][N] bf16, pitch ldy; sharing memory with x, W or preact is
- *           refused (QKN_ERR_UNSUPPORTED), columns of one wider buffer are fine
+ * y         [M][N] bf16, pitch ldy; sharing memory with x, W, preact, bias
+ *           or inv_rms is refused (QKN_ERR_UNSUPPORTED), columns of one wider
+ *           buffer are fine
  * bias      [N] of bias_dt, or NULL
  * residual  [M][N] bf16, pitch ldr, or NULL; may be y itself (the result is
  *           then added in place)
  * inv_rms   [M] fp32 row scale (flashnorm_inv_rms, with W folded by
  *           flashnorm_fold_weights), or NULL for 1
  * preact    [M][N] bf16, pitch ldz, receives z for linear_fused_backward, or
- *           NULL; sharing memory with x, W or residual is refused
+ *           NULL; sharing memory with any operand is refused
  * M >= 0, N and K multiples of 8, each below 2^31 - 512; pitches multiples of
  * 8; x, W, y, bias, residual and preact 16-byte aligned.  One launch, nothing is allocated.
  * The same call gives the same bits; the order in which K is added up goes by
@@ -514,7 +517,8 @@ QKN_API qkn_status linear_fused(const void *x, const void *W, void *y,
  *         (QKN_ERR_UNSUPPORTED).  M == 0 writes zeros to dW and dbias
  * workspace  at least linear_fused_backward_workspace_bytes(M, N, K, act)
  *         bytes of device scratch, 16-byte aligned, or NULL to allocate it
- *         stream-ordered inside the call
+ *         stream-ordered inside the call; sharing the bytes that are needed
+ *         with an input or a result is refused
  */
 QKN_API qkn_status linear_fused_backward(const void *dy, const void *preact, const void *x, const void *W,
                                          void *dx, void *dW, float *dbias,

@@ -204,10 +204,11 @@ qkn_status product(const pair::Matrix &a, const pair::Matrix &b, const pair::Mat
 
 bool pitch_ok(int64_t ld, int64_t width) { return ld >= width && ld % 8 == 0; }
 
-// Whether the rows of a bf16 result share memory with those of another matrix.
-bool meets(const pair::Matrix &y, const pair::Matrix &m) {
-    return rows_overlap({y.p, y.rows, y.inner * 2, y.pitch * 2}, {m.p, m.rows, m.inner * 2, m.pitch * 2});
-}
+Span span_of(const pair::Matrix &m) { return {m.p, m.rows, m.inner * 2, m.pitch * 2}; }
+
+// Whether the rows of a bf16 result share memory with those of another matrix, or with a vector.
+bool meets(const pair::Matrix &y, const pair::Matrix &m) { return rows_overlap(span_of(y), span_of(m)); }
+bool meets(const pair::Matrix &y, const Span &v) { return rows_overlap(span_of(y), v); }
 
 }  // namespace lin
 
@@ -251,9 +252,11 @@ extern "C" QKN_API qkn_status linear_fused(const void *x, const void *W, void *y
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const lin::pair::Matrix mx = {x, M, K, ldx}, mw = {W, N, K, ldw}, my = {y, M, N, ldy}, mr = {residual, M, N, ldr},
                             mz = {preact, M, N, ldz};
+    const Span vb = flat(bias, N * (int64_t)dtype_size(bias_dt)), vr = flat(inv_rms, 4 * M);
     const bool in_place = residual == y && (M == 1 || ldr == ldy);
     if (lin::meets(my, mx) || lin::meets(my, mw) || lin::meets(my, mz) || (lin::meets(my, mr) && !in_place) ||
-        lin::meets(mz, mx) || lin::meets(mz, mw) || lin::meets(mz, mr))
+        lin::meets(mz, mx) || lin::meets(mz, mw) || lin::meets(mz, mr) || lin::meets(my, vb) || lin::meets(my, vr) ||
+        lin::meets(mz, vb) || lin::meets(mz, vr))
         return fail(QKN_ERR_UNSUPPORTED, "%s: y or preact shares memory with an input or with one another", fn);
     const lin::pair::Matrix *res = residual ? &mr : nullptr, *z = preact ? &mz : nullptr;
     lin::Epilogue e{};
@@ -321,10 +324,15 @@ extern "C" QKN_API qkn_status linear_fused_backward(const void *dy, const void *
         bool met = lin::meets(results[0], results[1]);
         for (const lin::pair::Matrix &r : results)
             for (const lin::pair::Matrix &m : inputs) met = met || lin::meets(r, m);
-        const lin::pair::Matrix sums = {dbias, 1, 2 * N, 2 * N};  // N floats as bf16
-        for (const lin::pair::Matrix &r : results) met = met || lin::meets(sums, r);
-        for (const lin::pair::Matrix &m : inputs) met = met || lin::meets(sums, m);
+        const Span sums = flat(dbias, 4 * N);
+        for (const lin::pair::Matrix &r : results) met = met || lin::meets(r, sums);
+        for (const lin::pair::Matrix &m : inputs) met = met || lin::meets(m, sums);
         if (met) return fail(QKN_ERR_UNSUPPORTED, "%s: dx, dW or dbias shares memory with an input or with one another", fn);
+        const Span ws = flat(workspace, (int64_t)need);  // written before the products read their operands
+        met = rows_overlap(ws, sums);
+        for (const lin::pair::Matrix &r : results) met = met || lin::meets(r, ws);
+        for (const lin::pair::Matrix &m : inputs) met = met || lin::meets(m, ws);
+        if (met) return fail(QKN_ERR_UNSUPPORTED, "%s: the workspace shares memory with an input or a result", fn);
     }
     void *own = nullptr;
     if (workspace == nullptr && (has_z || dbias != nullptr)) {

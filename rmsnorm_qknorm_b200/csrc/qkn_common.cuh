@@ -52,6 +52,9 @@ inline bool same_rows(const Span &a, const Span &b) {
     return a.p == b.p && a.rows == b.rows && a.bytes == b.bytes && (a.rows <= 1 || a.pitch == b.pitch);
 }
 
+// A vector or a workspace of `bytes`.
+inline Span flat(const void *p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+
 inline size_t dtype_size(qkn_dtype t) { return t == QKN_F32 ? 4 : 2; }
 
 inline bool valid_dtype(int t) { return t == QKN_F32 || t == QKN_BF16; }

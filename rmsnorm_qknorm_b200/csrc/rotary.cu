@@ -381,8 +381,15 @@ qkn_status check_rotary_pointers(const char *fn, const void *positions, int pos_
 }
 
 // The results are the operand's own rows (in place) or rows that share nothing with any operand,
-// and not one another's: rows are read ahead of the ones that are written.
-qkn_status check_rotary_rows(const char *fn, const Args &a, int64_t es, bool inplace) {
+// and not one another's: rows are read ahead of the ones that are written.  Nor do they share anything
+// with the weights (of ws bytes), positions and frequencies, which other blocks may read later, or
+// with the workspace.
+qkn_status check_rotary_rows(const char *fn, const Args &a, int64_t es, int64_t ws, bool inplace,
+                             const void *workspace = nullptr, size_t workspace_bytes = 0) {
+    const Span pos = flat(a.r ? a.pos : nullptr, a.T * (a.pos64 ? 8 : 4)), freq = flat(a.r ? a.freq : nullptr, a.r / 2 * 8);
+    const Span scratch = flat(workspace, (int64_t)workspace_bytes);
+    if (rows_overlap(scratch, pos) || rows_overlap(scratch, freq))
+        return fail(QKN_ERR_UNSUPPORTED, "%s: the workspace shares memory with an input", fn);
     for (int i = 0; i < a.njobs; ++i) {
         const Job &j = a.job[i];
         const Span y = {j.y, a.T, j.d * es, j.ldy};
@@ -392,10 +399,19 @@ qkn_status check_rotary_rows(const char *fn, const Args &a, int64_t es, bool inp
             if ((rows_overlap(y, x) && !(inplace && o == i && same_rows(y, x))) || rows_overlap(y, g) ||
                 (o > i && rows_overlap(y, z)))
                 return fail(QKN_ERR_UNSUPPORTED, "%s: a result shares memory with an input or the other result", fn);
-            const Span w = {j.dw, 1, 4 * (int64_t)j.d, 0}, v = {k.dw, 1, 4 * (int64_t)k.d, 0};  // of gradients
+            const Span w = flat(j.dw, 4 * (int64_t)j.d), v = flat(k.dw, 4 * (int64_t)k.d);  // of gradients
             if (rows_overlap(w, x) || rows_overlap(w, g) || rows_overlap(w, z) || (o > i && rows_overlap(w, v)))
                 return fail(QKN_ERR_UNSUPPORTED, "%s: the gradient of weights shares memory with rows or the other's", fn);
+            const Span norm = flat(k.w, k.d * ws);
+            if (rows_overlap(y, norm) || rows_overlap(w, norm))
+                return fail(QKN_ERR_UNSUPPORTED, "%s: a result shares memory with weights", fn);
+            if (rows_overlap(scratch, x) || rows_overlap(scratch, g) || rows_overlap(scratch, z) ||
+                rows_overlap(scratch, v) || rows_overlap(scratch, norm))
+                return fail(QKN_ERR_UNSUPPORTED, "%s: the workspace shares memory with an input or a result", fn);
         }
+        const Span w = flat(j.dw, 4 * (int64_t)j.d);
+        if (rows_overlap(y, pos) || rows_overlap(y, freq) || rows_overlap(w, pos) || rows_overlap(w, freq))
+            return fail(QKN_ERR_UNSUPPORTED, "%s: a result shares memory with positions or frequencies", fn);
     }
     return QKN_OK;
 }
@@ -431,7 +447,7 @@ extern "C" QKN_API qkn_status rotary_apply(const void *q, const void *k, void *q
     a.job[1] = {static_cast<const uint8_t *>(k), nullptr, static_cast<uint8_t *>(k_out ? k_out : const_cast<void *>(k)),
                 nullptr, nullptr, ldk * e, 0, (k_out ? ldk_out : ldk) * e, (int)dk};
     a.njobs = has_k ? 2 : 1;
-    if (qkn_status st = rot::check_rotary_rows(fn, a, e, true)) return st;
+    if (qkn_status st = rot::check_rotary_rows(fn, a, e, e, true)) return st;
     return rot::launch_types<rot::kRotate>(a, act, act, static_cast<cudaStream_t>(stream));
 }
 
@@ -464,7 +480,7 @@ extern "C" QKN_API qkn_status qknorm_rotary(const void *q, const void *k, const 
     a.job[1] = {static_cast<const uint8_t *>(k), nullptr, static_cast<uint8_t *>(k_out ? k_out : const_cast<void *>(k)),
                 wk, nullptr, ldk * e, 0, (k_out ? ldk_out : ldk) * e, (int)dk};
     a.njobs = has_k ? 2 : 1;
-    if (qkn_status st = rot::check_rotary_rows(fn, a, e, true)) return st;
+    if (qkn_status st = rot::check_rotary_rows(fn, a, e, (int64_t)dtype_size(wdt), true)) return st;
     return rot::launch_types<rot::kNorm>(a, act, wdt, static_cast<cudaStream_t>(stream));
 }
 
@@ -525,7 +541,7 @@ extern "C" QKN_API qkn_status qknorm_rotary_backward(
     a.job[1] = {static_cast<const uint8_t *>(k), static_cast<const uint8_t *>(dk_out), static_cast<uint8_t *>(dk_in), wk,
                 dwk, ldk * e, ldgk * e, lddk * e, (int)dk};
     a.njobs = has_k ? 2 : 1;
-    if (qkn_status st = rot::check_rotary_rows(fn, a, e, false)) return st;
+    if (qkn_status st = rot::check_rotary_rows(fn, a, e, (int64_t)dtype_size(wdt), false, workspace, need)) return st;
     void *own = nullptr;
     if (workspace == nullptr) {
         const cudaError_t f = cudaMallocAsync(&own, need, s);
