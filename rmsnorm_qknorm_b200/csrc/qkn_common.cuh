@@ -27,8 +27,26 @@ struct Span {
     int64_t rows, bytes, pitch;
 };
 
+// sum over 0 <= i < n of floor((a i + b) / m), in a number of steps logarithmic in a and m: whole
+// parts of a / m and b / m add up directly, what is left counts the lattice points under a line, with
+// the axes exchanged.
+inline unsigned __int128 floor_sum(unsigned __int128 n, unsigned __int128 m, unsigned __int128 a, unsigned __int128 b) {
+    unsigned __int128 sum = 0;
+    while (true) {
+        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+        a %= m;
+        const unsigned __int128 top = a * n + b % m;
+        if (top < m) return sum;
+        n = top / m;
+        b = top % m;
+        const unsigned __int128 t = a;
+        a = m;
+        m = t;
+    }
+}
+
 // Whether any row of a shares a byte with a row of b.  Columns of one wider buffer do not, although
-// their address ranges cross.
+// their address ranges cross.  Never a walk over the rows, of which a call may have 2^31.
 inline bool rows_overlap(const Span &a, const Span &b) {
     using wide = __int128;  // pitches are the caller's: rows * pitch may pass 64 bits
     if (a.p == nullptr || b.p == nullptr || a.rows < 1 || b.rows < 1 || a.bytes < 1 || b.bytes < 1) return false;
@@ -39,12 +57,18 @@ inline bool rows_overlap(const Span &a, const Span &b) {
         const wide at = (b0 % a.pitch + a.pitch) % a.pitch;  // where b's rows begin in a's
         return at < a.bytes || at + b.bytes > a.pitch;
     }
-    for (int64_t i = 0; i < a.rows; ++i) {
-        const wide start = (wide)i * a.pitch, before = start - b0 - b.bytes;
-        const wide j = before < 0 ? 0 : before / b.pitch + 1;  // b's first row that ends behind the start of a's row i
-        if (j < b.rows && b0 + j * b.pitch < start + a.bytes) return true;
-    }
-    return false;
+    // a's rows between b's first byte and its last one.  One of them that meets b's rows continued in
+    // both directions meets b itself: the row before b's first one, or behind its last one, is met
+    // only together with that one.  Row i meets as many rows as there are j with
+    // i pa - bytes(b) < b0 + j pb < i pa + bytes(a).
+    const wide pa = a.rows > 1 ? a.pitch : 1, pb = b.rows > 1 ? b.pitch : 1;
+    const wide first = a.rows == 1 || b0 < a.bytes ? 0 : (b0 - a.bytes) / pa + 1;
+    const wide end = a.rows == 1 ? 1 : (b0 + (b.rows - 1) * pb + b.bytes - 1) / pa + 1;  // behind the last one
+    const wide n = (end < a.rows ? end : a.rows) - first;
+    if (n < 1) return false;
+    const wide at = first * pa - b0, low = at - b.bytes, high = at + a.bytes - 1;
+    const wide up = low < 0 ? (-low / pb + 1) * pb : 0;  // whole rows, so that nothing is negative
+    return floor_sum(n, pb, pa, high + up) != floor_sum(n, pb, pa, low + up);
 }
 
 // The same rows: a result that replaces its operand in place.

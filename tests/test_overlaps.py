@@ -123,3 +123,40 @@ def test_rotary_results_beside_others_pass(lib):
     assert qknorm(lib, r=0, pos=3 * P, freq=3 * P) == CUDA  # not read without a rotation
     assert back(lib) == CUDA and back(lib, dwq=7 * P + 256, dwk=8 * P - 256) == CUDA
     assert back(lib, ws=3 * P + 1024) == CUDA and back(lib, ws=5 * P + 32) == CUDA
+
+
+def meets(a, b):
+    """Whether rows (start, rows, bytes, pitch) share a byte, byte by byte."""
+    return bool(set(a[0] + i * a[3] + c for i in range(a[1]) for c in range(a[2]))
+                & set(b[0] + i * b[3] + c for i in range(b[1]) for c in range(b[2])))
+
+
+@no_gpu
+def test_rows_under_other_pitches_against_every_byte(lib):
+    # q's rows and k's result, both of small widths and pitches, among one another in all ways; the rest lies far away
+    import random
+    rng, met = random.Random(5), 0
+    for _ in range(4000):
+        T, dq, dk = rng.randint(1, 9), 2 * rng.randint(1, 5), 2 * rng.randint(1, 5)
+        lq, lk = dq + rng.choice([0, 0, 1, 2, 7, rng.randint(0, 60)]), dk + rng.choice([0, 1, 2, 5, rng.randint(0, 60)])
+        at = 64 * P + 2 * rng.randint(-T * lk - 4, T * lq + 4)
+        st = lib.rotary_apply(64 * P, P, 2 * P, at, T, dq, dk, lq, dk, dq, lk, 2, 4 * P, 64, 5 * P, 2, 0, 1.0, 0, BF16, None)
+        hit = meets((64 * P, T, 2 * dq, 2 * lq), (at, T, 2 * dk, 2 * lk))
+        met += hit
+        assert st == (UNSUP if hit else CUDA), (T, dq, dk, lq, lk, at - 64 * P)
+    assert 400 < met < 3600
+
+
+@no_gpu
+def test_many_rows_under_two_pitches_are_checked_at_once(lib):
+    # every 32 bytes against every 48, apart from one another (a walk over 2^28 rows takes seconds)
+    import time
+    T, A = 1 << 28, 1 << 40
+
+    def call(at):
+        return lib.rotary_apply(A, None, at, None, T, 2, 0, 16, 0, 24, 0, 2, 1 << 50, 64, 1 << 52, 2, 0, 1.0, 0, BF16, None)
+
+    t0 = time.perf_counter()
+    assert call(A + 8) == CUDA and time.perf_counter() - t0 < 0.5
+    # the last row of q_out alone reaches the first one of q
+    assert call(A + 8 - 48 * (T - 1)) == CUDA and call(A + 2 - 48 * (T - 1)) == UNSUP
