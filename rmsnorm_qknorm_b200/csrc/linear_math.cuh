@@ -95,7 +95,8 @@ template <int ACT> __device__ __forceinline__ float2 slope2(float2 z) {
         return __ffma2_rn(z, __fmul2_rn(gauss, pair_of(0.39894228040143268f)), cdf);
     }
     if constexpr (ACT == QKN_ACT_GELU_TANH) {
-        const float2 zz = __fmul2_rn(z, z);
+        // z^2 is cut where p (1 - p) has long been zero, so that its overflow (|z| above 1.8e19) does not meet that zero
+        const float2 sq = __fmul2_rn(z, z), zz = make_float2(fminf(sq.x, 1e8f), fminf(sq.y, 1e8f));
         const float2 w = __ffma2_rn(zz, pair_of(-kLog2e * kTanhA * kTanhB), pair_of(-kLog2e * kTanhA));
         const float2 p = logistic2(__fmul2_rn(z, w));
         const float2 r = __ffma2_rn(p, pair_of(-1.f), pair_of(1.f));
