@@ -398,7 +398,10 @@ typedef enum {
  * turns back (the sine's sign is flipped, mscale is still applied): the
  * gradient of the call without it.  fp32 arithmetic, one rounding to `act`.  Any element-aligned
  * pointers and pitches are accepted; 16-byte aligned rows of whole 16 bytes
- * with head_dim a multiple of 4 and rotary_dim of 8 take the fast kernel.
+ * with head_dim a multiple of 4 and rotary_dim of 8 take the fast kernel, up
+ * to about 30000 elements of q and k together (15000 in fp32 or where only 8
+ * bytes divide a bf16 head's parts).  The same holds for the two calls below;
+ * gradients take it up to about 15000 elements.
  */
 QKN_API qkn_status rotary_apply(const void *q, const void *k, void *q_out, void *k_out,
                                 int64_t T, int64_t dq, int64_t dk,

@@ -777,8 +777,9 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
     p.rot_units = a.r / (2 * E);
     const int u0 = p.job[0].nunits, u1 = a.njobs > 1 ? p.job[1].nunits : 0;
     auto warps_of = [](int units, int upt) { return (units + 32 * upt - 1) / (32 * upt); };
-    // Two units of 16 bf16 elements or four of 8 fp32 a thread, twice that for rows too wide
-    // otherwise.  (Half of it leaves fewer groups to an SM, and it is the groups that hide one
+    // Two units of 16 bf16 elements or four of 8 fp32 a thread, twice that in bf16 forward calls for
+    // rows too wide otherwise; what 15 warps then do not hold (15360 elements of q and k together, or
+    // 30720) the element-wise kernel serves.  (Half of it leaves fewer groups to an SM, and it is the groups that hide one
     // another's barriers: 16384 x (5120 + 1024) bf16, gradients 145 against 118 us, rotary alone 93
     // against 67.)  Warps serve both tensors where nothing is summed over a row, or where one warp
     // is enough.
