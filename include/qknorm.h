@@ -368,7 +368,7 @@ QKN_API qkn_status flashnorm_proj_noalloc(const void *x, const void *W_folded, v
  *   c = mscale * cos(theta), s = mscale * sin(theta)
  *   y_a = x_a c - x_b s,  y_b = x_b c + x_a s
  * The angle is formed in fp64 and reduced to less than a turn before cos and
- * sin are taken in fp32: its error is 2^-52 of the angle before the
+ * sin are taken in fp32: its error is below 2^-51 of the angle before the
  * reduction, less than fp32 resolves up to 10^8 radians.  No table is read or
  * kept.
  *

@@ -558,7 +558,7 @@ qkn_status make_tmap_store(CUtensorMap *m, void *ptr, int64_t rows, int64_t cols
 }
 
 qkn_status make_tmap_pitched(CUtensorMap *m, const void *ptr, int64_t rows, int64_t inner, int64_t pitch,
-                             int box_inner, int box_rows, int swizzle_bytes) {
+                             int box_inner, int box_rows) {
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return fail(QKN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
     cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
@@ -566,9 +566,8 @@ qkn_status make_tmap_pitched(CUtensorMap *m, const void *ptr, int64_t rows, int6
     cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(QKN_ERR_CUDA, "cuTensorMapEncodeTiled (pitched) failed (CUresult %d)", (int)r);
     return QKN_OK;
 }

@@ -87,9 +87,9 @@ qkn_status make_tmap(CUtensorMap *m, const void *ptr, int64_t rows, int64_t inne
 qkn_status make_tmap_store(CUtensorMap *m, void *ptr, int64_t rows, int64_t cols);
 
 // 2-D bf16 tensor [rows][inner], rows `pitch` elements apart, as a TMA tensor
-// map of box_inner x box_rows boxes with a 64- or 128-byte swizzle.
+// map of box_inner x box_rows boxes with a 128-byte swizzle.
 qkn_status make_tmap_pitched(CUtensorMap *m, const void *ptr, int64_t rows, int64_t inner, int64_t pitch,
-                             int box_inner, int box_rows, int swizzle_bytes);
+                             int box_inner, int box_rows);
 
 // inv[m] = 1/sqrt(sum_k x[m][k]^2 / K + eps) for bf16 x [M][K] (K a multiple
 // of 8, rows 16-byte aligned), on stream s.

@@ -113,17 +113,5 @@ struct Epilogue {
     int bias_bf16;
 };
 
-// Bias of 8 columns (16-byte aligned), 0 without one.
-__device__ __forceinline__ void load_bias8(const Epilogue &e, int col, float (&b)[8]) {
-    if (e.bias == nullptr) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = 0.f;
-    } else if (e.bias_bf16) {
-        load_weights_batched<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16 *>(e.bias) + col, b);
-    } else {
-        load_weights_batched<float, 8>(static_cast<const float *>(e.bias) + col, b);
-    }
-}
-
 }  // namespace lin
 }  // namespace qkn

@@ -10,8 +10,9 @@
 // of each operand per CTA, as 128-byte-swizzled rows of 64 k, or as two
 // blocks of 64 (k) rows of 64 m.
 //
-// Roles per CTA (320 threads): warp 0 moves tiles with TMA, one lane of the
-// even CTA's warp 1 issues the MMAs, warps 2-9 run the epilogue of a tile
+// Roles per CTA (320 threads): warp 0 moves tiles with TMA, the even CTA's
+// warp 1 issues the MMAs (both as whole warps with an elected lane, see
+// linear_issue.cuh), warps 2-9 run the epilogue of a tile
 // while the MMAs of the next one run into the other accumulator: a quarter of
 // the rows and every other 64 columns per warp, a row per thread: accumulator
 // -> times the row's scale, plus bias -> z (stored where asked) -> activation
@@ -396,12 +397,12 @@ qkn_status launch_bn(const Matrix &a, const Matrix &b, const Matrix &y, const Ma
     using S = Shape<BN>;
     const auto kernel = linear_pair_kernel<A_MN, B_MN, BN, ACT>;
     CUtensorMap ta, tb, ty, tr;
-    if (qkn_status st = make_tmap_pitched(&ty, y.p, y.rows, y.inner, y.pitch, BOX_COLS, 32, 128)) return st;
+    if (qkn_status st = make_tmap_pitched(&ty, y.p, y.rows, y.inner, y.pitch, BOX_COLS, 32)) return st;
     tr = ty;
     if (res != nullptr)
-        if (qkn_status st = make_tmap_pitched(&tr, res->p, res->rows, res->inner, res->pitch, BOX_COLS, 32, 128)) return st;
-    if (qkn_status st = make_tmap_pitched(&ta, a.p, a.rows, a.inner, a.pitch, BK, A_MN ? BK : BM, 128)) return st;
-    if (qkn_status st = make_tmap_pitched(&tb, b.p, b.rows, b.inner, b.pitch, BK, B_MN ? BK : S::BN_CTA, 128)) return st;
+        if (qkn_status st = make_tmap_pitched(&tr, res->p, res->rows, res->inner, res->pitch, BOX_COLS, 32)) return st;
+    if (qkn_status st = make_tmap_pitched(&ta, a.p, a.rows, a.inner, a.pitch, BK, A_MN ? BK : BM)) return st;
+    if (qkn_status st = make_tmap_pitched(&tb, b.p, b.rows, b.inner, b.pitch, BK, B_MN ? BK : S::BN_CTA)) return st;
     g.pm_blocks = (int)(((int64_t)g.M + 2 * BM - 1) / (2 * BM));
     g.n_blocks = (int)(((int64_t)g.N + BN - 1) / BN);
     g.k_blocks = (int)((K + BK - 1) / BK);

@@ -281,8 +281,8 @@ template <int BT, int ACT, bool F_MN, bool T_MN>
 qkn_status launch_bt(const pair::Matrix &x, const pair::Matrix &W, const Args &a, cudaStream_t s) {
     const auto kernel = linear_rows_kernel<BT, ACT, F_MN, T_MN>;
     CUtensorMap tw, tx;
-    if (qkn_status st = make_tmap_pitched(&tw, W.p, W.rows, W.inner, W.pitch, BK, F_MN ? BK : BF, 128)) return st;
-    if (qkn_status st = make_tmap_pitched(&tx, x.p, x.rows, x.inner, x.pitch, BK, T_MN ? BK : BT, 128)) return st;
+    if (qkn_status st = make_tmap_pitched(&tw, W.p, W.rows, W.inner, W.pitch, BK, F_MN ? BK : BF)) return st;
+    if (qkn_status st = make_tmap_pitched(&tx, x.p, x.rows, x.inner, x.pitch, BK, T_MN ? BK : BT)) return st;
     static std::atomic<bool> attr_set[64];  // per device: the attribute has been set
     int dev = 0;
     cudaGetDevice(&dev);

@@ -170,8 +170,8 @@ template <bool A_MN, bool B_MN, int BN, int ACT>
 qkn_status launch_bn(const pair::Matrix &x, const pair::Matrix &W, const rows::Args &a, int parts, cudaStream_t s) {
     const auto kernel = linear_split_kernel<A_MN, B_MN, BN, ACT>;
     CUtensorMap ta, tb;
-    if (qkn_status st = make_tmap_pitched(&ta, x.p, x.rows, x.inner, x.pitch, BK, A_MN ? BK : BM, 128)) return st;
-    if (qkn_status st = make_tmap_pitched(&tb, W.p, W.rows, W.inner, W.pitch, BK, B_MN ? BK : BN / 2, 128)) return st;
+    if (qkn_status st = make_tmap_pitched(&ta, x.p, x.rows, x.inner, x.pitch, BK, A_MN ? BK : BM)) return st;
+    if (qkn_status st = make_tmap_pitched(&tb, W.p, W.rows, W.inner, W.pitch, BK, B_MN ? BK : BN / 2)) return st;
     static std::atomic<bool> attr_set[64];  // per device: the attribute has been set
     int dev = 0;
     cudaGetDevice(&dev);

@@ -46,7 +46,6 @@ __device__ int g_rotary_error = 0;
 namespace rot {
 namespace unit {
 
-constexpr int kMaxThreads = 512;
 constexpr int kSmemLimit = 227 * 1024;
 
 struct Rows {
