@@ -6,6 +6,9 @@
 // linear_pair.cuh for many, linear_split.cuh between) with everything else in
 // their epilogue; dz is formed once (and rounded to bf16, the products'
 // operand type) by an element-wise pass that adds up db in fp32 on the way.
+// That rounding takes dx and dW from 1.7 x 10^-3 of their norm off the 64-bit
+// result (their own rounding alone) to 2.3 x 10^-3 at 4096 x 12288 x 4096; dz as
+// a sum of two bf16 parts would double the time of both products.
 #include <algorithm>
 #include <atomic>
 #include <cuda.h>

@@ -316,7 +316,9 @@ qkn_status launch_bt(const pair::Matrix &x, const pair::Matrix &W, const Args &a
 // About how long the kernel takes with bt tokens per tile, in ns: 3.5 us, and for each of the CTAs
 // that share an SM its blocks of 64 k (c below) and the 25 ns a token takes in the last step.
 // Measured like pair::cost; it leaves out the weights' way from DRAM, which is the same for
-// every bt and sets the time of few tokens and many features.
+// every bt and sets the time of few tokens and many features, and how many clusters the device holds
+// at once: 768 x 1024 x 1024, 48 tiles in clusters of three, takes 10.5 us with gelu where this says
+// 7.4 (512 rows in clusters of four 7.9 and 6.2, 1024 rows by the split kernel 9.5).
 inline int64_t cost(int64_t M, int64_t N, int64_t K, int bt) {
     const int64_t sms = sm_count(), kb = (K + BK - 1) / BK, tiles = ((N + BF - 1) / BF) * ((M + bt - 1) / bt);
     const int64_t c = bt == 16 ? 190 : bt == 32 ? 200 : bt == 64 ? 300 : 480;

@@ -778,7 +778,7 @@ Plan plan(const Args &a, Params &p, size_t w_size) {
     auto warps_of = [](int units, int upt) { return (units + 32 * upt - 1) / (32 * upt); };
     // Two units of 16 bf16 elements or four of 8 fp32 a thread, twice that in bf16 forward calls for
     // rows too wide otherwise; what 15 warps then do not hold (15360 elements of q and k together, or
-    // 30720) the element-wise kernel serves.  (Half of it leaves fewer groups to an SM, and it is the groups that hide one
+    // twice that) the element-wise kernel serves.  (Half of it leaves fewer groups to an SM, and it is the groups that hide one
     // another's barriers: 16384 x (5120 + 1024) bf16, gradients 145 against 118 us, rotary alone 93
     // against 67.)  Warps serve both tensors where nothing is summed over a row, or where one warp
     // is enough.

@@ -1,7 +1,7 @@
 """Rows wider than 15 warps of two units a thread: four units a thread (bf16, forward calls), the element-wise kernels.
 
-The limits of the kernels, per token of q and k together: 30720 elements (bf16 forward), 15360 (fp32, gradients, bf16
-heads of 8-byte chunks), less where q or k does not fill its last warp, and what shared memory holds.
+The limits of the kernels, per token of q and k together: 15360 elements (fp32, gradients, bf16 heads of 8-byte
+chunks) or twice that (bf16 forward), less where q or k does not fill its last warp, and what shared memory holds.
 """
 from __future__ import annotations
 
