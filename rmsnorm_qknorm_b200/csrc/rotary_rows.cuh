@@ -859,7 +859,7 @@ qkn_status launch_layout(Params &p, const Plan &r, int layout, int *grid, cudaSt
 // not: then the weights lie in the order of the units, and where a power of two of units leaves the
 // first chunks in half of the banks, every other four (eight) units take their second chunk first.
 // 32768 x (4096 + 1024) bf16, norm and gradients: heads of 64 137 -> 114 and 241 -> 193 us, of 96
-// 142 -> 125 and 237 -> 206; heads of 128 lose (108 -> 109, 188 -> 194).  Rotary alone, which reads
+// (3840 + 960) 142 -> 125 and 237 -> 206; heads of 128 lose (108 -> 109, 188 -> 194).  Rotary alone, which reads
 // a chunk once, runs at the copy's rate without.
 template <int CB>
 bool ordered_of(Params &p) {
