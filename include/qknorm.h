@@ -373,6 +373,7 @@ QKN_API qkn_status flashnorm_proj_noalloc(const void *x, const void *W_folded, v
  * kept.
  *
  * T          below 2^31
+ * dq, dk     at most 2^30 - 16
  * positions  [T] int32 (pos_bits 32) or int64 (64), any values, in any order
  * inv_freq   [rotary_dim / 2] fp64, radians per position.  Frequencies that
  *            are scaled for longer contexts are given here as they are

@@ -32,6 +32,7 @@ namespace rot {
 
 constexpr int kMaxRotary = 1024;      // rotated elements per head at most (the cos / sin table of a row)
 constexpr int kBlock = 256;
+constexpr int64_t kMaxWidth = 0x3ffffff0;  // of a row: columns of q and k, rounded up to blocks of 32, stay below 2^31
 
 // One tensor of the call: query or key rows.
 struct Job {
@@ -341,7 +342,7 @@ qkn_status check_rotary(const char *fn, int64_t T, int64_t dq, int64_t dk, int64
                         int pos_bits, int layout, float mscale, qkn_dtype act, qkn_dtype wdt) {
     if (!valid_dtype(act) || !valid_dtype(wdt))
         return fail(QKN_ERR_DTYPE, "%s: unknown dtype (act=%d, wdt=%d)", fn, (int)act, (int)wdt);
-    if (T < 0 || dq < 1 || dk < 0 || dq > 0x3fffffffLL || dk > 0x3fffffffLL || T > 0x7fffffffLL)
+    if (T < 0 || dq < 1 || dk < 0 || dq > kMaxWidth || dk > kMaxWidth || T > 0x7fffffffLL)
         return fail(QKN_ERR_SHAPE, "%s: bad sizes T=%lld dq=%lld dk=%lld", fn, (long long)T, (long long)dq,
                     (long long)dk);
     if (rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > kMaxRotary)
@@ -490,7 +491,7 @@ extern "C" QKN_API qkn_status qknorm_rotary(const void *q, const void *k, const 
 }
 
 extern "C" QKN_API size_t qknorm_rotary_backward_workspace_bytes(int64_t T, int64_t dq, int64_t dk) {
-    if (T < 0 || dq < 1 || dk < 0 || dq > 0x3fffffffLL || dk > 0x3fffffffLL || T > 0x7fffffffLL) return 0;
+    if (T < 0 || dq < 1 || dk < 0 || dq > rot::kMaxWidth || dk > rot::kMaxWidth || T > 0x7fffffffLL) return 0;
     // row factors of both tensors (element-wise kernels), then rows of partial sums: one per
     // slice of the element-wise kernel or per block of the unit kernel
     const size_t inv = ((size_t)T * 2 * 4 + 255) / 256 * 256;

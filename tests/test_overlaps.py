@@ -1,4 +1,4 @@
-"""Results and workspaces over what a call reads, on the host (no GPU needed: the addresses are made up).
+"""Results and workspaces over what a call reads, and limits of sizes, on the host (no GPU needed: the addresses are made up).
 
 Vectors (bias, row scales, norm weights, positions, frequencies) and the workspace, beside the rows that
 test_linear.py and test_rotary.py cover.  A call that only touches its neighbours is not refused; without a GPU it
@@ -160,3 +160,18 @@ def test_many_rows_under_two_pitches_are_checked_at_once(lib):
     assert call(A + 8) == CUDA and time.perf_counter() - t0 < 0.5
     # the last row of q_out alone reaches the first one of q
     assert call(A + 8 - 48 * (T - 1)) == CUDA and call(A + 2 - 48 * (T - 1)) == UNSUP
+
+
+@no_gpu
+def test_the_widest_rows(lib):
+    # the columns of q and k together, rounded up to the blocks that add up the weights' gradients, fit 31 bits
+    A, W = 1 << 40, (1 << 30) - 16
+
+    def call(dq, dk):
+        at = [A + (i << 33) for i in range(13)]
+        return lib.qknorm_rotary_backward(*at[:10], 1, dq, dk, dq, dk, dq, dk, dq, dk, 2, at[10], 64, at[11], 2, 0, 1.0, BF16,
+                                          BF16, 1e-6, None, 0, None)
+
+    assert call(W, W) == CUDA and call(W + 2, W) == SHAPE and call(W, W + 2) == SHAPE
+    assert lib.qknorm_rotary_backward_workspace_bytes(1, W, W) >= 8 * W
+    assert lib.qknorm_rotary_backward_workspace_bytes(1, W, W + 2) == 0
